@@ -251,6 +251,83 @@ moe_status moe_cache_stats(moe_layer* layer, uint64_t* hits, uint64_t* misses,
  * word (MOE_ERR_BOUNDS or MOE_ERR_TIMEOUT if a kernel recorded one). */
 moe_status moe_status_sync(moe_layer* layer, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the layer, for models that interleave moe_forward with
+ * their own layers: the norm that feeds it, and projections (attention's, the
+ * output head) with weights in the experts' format.  They follow the
+ * conventions above with these differences: every pointer must be device
+ * memory of the current device (or managed memory), aligned to 16 bytes (y,
+ * scales and bias: to their type); anything else, and buffers that overlap
+ * except where allowed, returns MOE_ERR_INVALID before any work is queued.
+ * No call allocates except moe_linear_create.  Each may run while the
+ * preceding kernel of its stream drains, but touches the caller's memory only
+ * after it. */
+
+/* Residual addition and RMS norm over rows of `hidden` values:
+ *   h = bf16(x + residual)                (h = x when residual is NULL)
+ *   u = h / sqrt(mean(h^2) + eps) * gain  (gain NULL: 1)
+ * with the mean in fp32 over the rounded h, as in moe_stack_forward (which
+ * has gain 1 and eps 1e-6).  x, residual, h, u: bf16 [n_tokens][hidden]; gain
+ * fp32 [hidden].  h may be NULL (not wanted).  h or u may be x or residual
+ * itself (not both the same buffer).  Limits: 32 <= hidden <= 32768, a
+ * multiple of 32; 1 <= n_tokens <= 65536; eps finite and >= 0. */
+moe_status moe_add_rmsnorm(const void* x_bf16, const void* residual_bf16, const float* gain,
+                           float eps, int n_tokens, int hidden, void* h_bf16, void* u_bf16,
+                           void* stream);
+
+/* The same with u in 8 bits, one fp32 scale per 32 values along the row:
+ *   scale = max|u| / 127 over the block, u_q8 = round(u / scale), ties to even
+ * u_q8 int8 [n_tokens][hidden] in -127..127, u_scale fp32
+ * [n_tokens][hidden/32].  A block whose max|u| is below 1e-30 is written as
+ * zeros with scale 0; one that holds an infinity or NaN as zeros with a NaN
+ * scale.  Only h may be x or residual itself. */
+moe_status moe_add_rmsnorm_q8(const void* x_bf16, const void* residual_bf16, const float* gain,
+                              float eps, int n_tokens, int hidden, void* h_bf16, int8_t* u_q8,
+                              float* u_scale, void* stream);
+
+typedef struct moe_linear moe_linear; /* opaque, owned by the library */
+
+/* Limits: 32 <= in_features <= 32768, a multiple of 32; 1 <= out_features <=
+ * 1048576; 1 <= max_tokens <= 65536. */
+typedef struct {
+  int32_t in_features;  /* K */
+  int32_t out_features; /* N */
+  int32_t max_tokens;   /* largest n_tokens any call will pass */
+} moe_linear_config;
+
+/* Packed like the experts' tensors: q [N][K/2] codes, s [N][K/32] binary16
+ * scales, weight = (nibble - 8) * scale; bias [N] fp32 or NULL. */
+typedef struct {
+  const uint8_t* q;
+  const uint16_t* s;
+  const float* bias;
+} moe_linear_weights;
+
+/* Creates a projection: validates cfg, allocates its HBM and packs the
+ * weights into the library's own layout.  weights_on_device, ownership and
+ * synchronisation as in moe_layer_create. */
+moe_status moe_linear_create(const moe_linear_config* cfg, const moe_linear_weights* w,
+                             int weights_on_device, moe_linear** out);
+
+/* Frees a projection (NULL is a no-op).  Synchronises the device first. */
+void moe_linear_destroy(moe_linear* linear);
+
+/* y = x W^T + bias: x bf16 [n_tokens][K], y bf16 [n_tokens][N], results
+ * bit-identical from call to call.  Calls on one handle must not overlap on
+ * the GPU.  A token with an infinity or NaN in x has unspecified non-finite
+ * values (or NaN) in y; other tokens are not affected. */
+moe_status moe_linear_forward(moe_linear* linear, const void* x_bf16, int n_tokens, void* y_bf16,
+                              void* stream);
+
+/* The decode form on 8-bit activations, as moe_add_rmsnorm_q8 writes them:
+ * x = x_q8 * x_scale, x_q8 int8 [n_tokens][K], x_scale fp32
+ * [n_tokens][K/32].  At most 32 tokens (more: MOE_ERR_CAPACITY). */
+moe_status moe_linear_forward_q8(moe_linear* linear, const int8_t* x_q8, const float* x_scale,
+                                 int n_tokens, void* y_bf16, void* stream);
+
+/* moe_status_sync for a projection. */
+moe_status moe_linear_status_sync(moe_linear* linear, void* stream);
+
 /* Per-kernel timing of the library's own launches, for measurement (off by
  * default; it adds two event records per launch).  While enabled, every
  * kernel launch is bracketed by CUDA events on its stream.

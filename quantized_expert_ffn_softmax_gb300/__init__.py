@@ -57,6 +57,15 @@ class moe_layer_weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in WEIGHT_FIELDS]
 
 
+class moe_linear_config(ctypes.Structure):
+    _fields_ = [("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32),
+                ("max_tokens", ctypes.c_int32)]
+
+
+class moe_linear_weights(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("s", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -99,6 +108,23 @@ def lib():
         L.moe_status_sync.restype = i32
         L.moe_cache_stats.argtypes = [vp, vp, vp, vp, i32, vp]
         L.moe_cache_stats.restype = i32
+        f32 = ctypes.c_float
+        L.moe_add_rmsnorm.argtypes = [vp, vp, vp, f32, i32, i32, vp, vp, vp]
+        L.moe_add_rmsnorm.restype = i32
+        L.moe_add_rmsnorm_q8.argtypes = [vp, vp, vp, f32, i32, i32, vp, vp, vp, vp]
+        L.moe_add_rmsnorm_q8.restype = i32
+        L.moe_linear_create.argtypes = [ctypes.POINTER(moe_linear_config),
+                                        ctypes.POINTER(moe_linear_weights), i32,
+                                        ctypes.POINTER(vp)]
+        L.moe_linear_create.restype = i32
+        L.moe_linear_destroy.argtypes = [vp]
+        L.moe_linear_destroy.restype = None
+        L.moe_linear_forward.argtypes = [vp, vp, i32, vp, vp]
+        L.moe_linear_forward.restype = i32
+        L.moe_linear_forward_q8.argtypes = [vp, vp, vp, i32, vp, vp]
+        L.moe_linear_forward_q8.restype = i32
+        L.moe_linear_status_sync.argtypes = [vp, vp]
+        L.moe_linear_status_sync.restype = i32
         _lib = L
     return _lib
 
@@ -243,6 +269,49 @@ def moe_status_sync(layer: int, stream=None) -> int:
     return lib().moe_status_sync(layer, _stream(stream))
 
 
+def moe_add_rmsnorm(x, residual, gain, eps: float, n_tokens: int, hidden: int, h, u,
+                    stream=None) -> None:
+    """h = bf16(x + residual), u = h / sqrt(mean(h^2) + eps) * gain, rows of `hidden`
+    values; residual, gain and h may be None."""
+    _check(lib().moe_add_rmsnorm(_ptr(x), _ptr(residual), _ptr(gain), eps, n_tokens, hidden,
+                                 _ptr(h), _ptr(u), _stream(stream)))
+
+
+def moe_add_rmsnorm_q8(x, residual, gain, eps: float, n_tokens: int, hidden: int, h, u_q8,
+                       u_scale, stream=None) -> None:
+    """moe_add_rmsnorm with u as int8 codes and one fp32 scale per 32 values."""
+    _check(lib().moe_add_rmsnorm_q8(_ptr(x), _ptr(residual), _ptr(gain), eps, n_tokens, hidden,
+                                    _ptr(h), _ptr(u_q8), _ptr(u_scale), _stream(stream)))
+
+
+def moe_linear_create(config: dict, weights: dict, weights_on_device: bool) -> int:
+    """Creates a projection; returns its opaque handle (an integer address)."""
+    cfg = moe_linear_config(config["in_features"], config["out_features"], config["max_tokens"])
+    w = moe_linear_weights(*[_ptr(weights.get(n)) for n in ("q", "s", "bias")])
+    out = ctypes.c_void_p()
+    _check(lib().moe_linear_create(ctypes.byref(cfg), ctypes.byref(w),
+                                   int(bool(weights_on_device)), ctypes.byref(out)))
+    return out.value
+
+
+def moe_linear_destroy(linear: int) -> None:
+    lib().moe_linear_destroy(linear)
+
+
+def moe_linear_forward(linear: int, x, n_tokens: int, y, stream=None) -> None:
+    _check(lib().moe_linear_forward(linear, _ptr(x), n_tokens, _ptr(y), _stream(stream)))
+
+
+def moe_linear_forward_q8(linear: int, x_q8, x_scale, n_tokens: int, y, stream=None) -> None:
+    _check(lib().moe_linear_forward_q8(linear, _ptr(x_q8), _ptr(x_scale), n_tokens, _ptr(y),
+                                       _stream(stream)))
+
+
+def moe_linear_status_sync(linear: int, stream=None) -> int:
+    """Synchronises and returns (and clears) the projection's device error word."""
+    return lib().moe_linear_status_sync(linear, _stream(stream))
+
+
 def moe_profile_enable(enable: bool) -> None:
     _check(lib().moe_profile_enable(int(bool(enable))))
 
@@ -297,6 +366,80 @@ class MoELayer:
         w = torch.empty((T, k), dtype=torch.float32, device=x.device)
         moe_route(self.handle, x, T, ids, w, stream)
         return ids, w
+
+
+def _rows(x, name, dtype, width=None):
+    """The row count of a 2-D device tensor of the given type (and row width)."""
+    if x.dim() != 2 or x.dtype != dtype or (width is not None and x.shape[1] != width):
+        raise ValueError("%s must be a 2-D %s tensor%s, not %s %s" % (
+            name, dtype, "" if width is None else " of %d columns" % width, tuple(x.shape),
+            x.dtype))
+    return x.shape[0]
+
+
+def add_rmsnorm(x, residual=None, gain=None, eps: float = 1e-6, q8: bool = False, stream=None):
+    """Residual addition and RMS norm of bf16 rows: (h, u), or with q8=True
+    (h, u_q8, u_scale).  Without a residual h is x itself."""
+    import torch
+
+    T, H = _rows(x, "x", torch.bfloat16), x.shape[1]
+    if residual is not None and _rows(residual, "residual", torch.bfloat16, H) != T:
+        raise ValueError("residual must have x's shape")
+    if gain is not None and (gain.dtype != torch.float32 or tuple(gain.shape) != (H,)):
+        raise ValueError("gain must be a float32 tensor of %d values" % H)
+    h = torch.empty_like(x) if residual is not None else None
+    if not q8:
+        u = torch.empty_like(x)
+        moe_add_rmsnorm(x, residual, gain, eps, T, H, h, u, stream)
+        return (x if h is None else h), u
+    q = torch.empty((T, H), dtype=torch.int8, device=x.device)
+    s = torch.empty((T, H // 32), dtype=torch.float32, device=x.device)
+    moe_add_rmsnorm_q8(x, residual, gain, eps, T, H, h, q, s, stream)
+    return (x if h is None else h), q, s
+
+
+class MoELinear:
+    """Owns one projection handle (weights in the experts' 4-bit format); the
+    calls allocate their output with torch."""
+
+    def __init__(self, config: dict, weights: dict, weights_on_device: bool):
+        self.config = dict(config)
+        self.handle = moe_linear_create(config, weights, weights_on_device)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            moe_linear_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _out(self, x, T):
+        import torch
+
+        return torch.empty((T, self.config["out_features"]), dtype=torch.bfloat16, device=x.device)
+
+    def forward(self, x, stream=None):
+        import torch
+
+        T = _rows(x, "x", torch.bfloat16, self.config["in_features"])
+        y = self._out(x, T)
+        moe_linear_forward(self.handle, x, T, y, stream)
+        return y
+
+    def forward_q8(self, x_q8, x_scale, stream=None):
+        import torch
+
+        K = self.config["in_features"]
+        T = _rows(x_q8, "x_q8", torch.int8, K)
+        if _rows(x_scale, "x_scale", torch.float32, K // 32) != T:
+            raise ValueError("x_q8 and x_scale must have as many rows")
+        y = self._out(x_q8, T)
+        moe_linear_forward_q8(self.handle, x_q8, x_scale, T, y, stream)
+        return y
 
 
 def stack_forward(layers: Sequence[MoELayer], x, stream=None, trace: bool = False):

@@ -1,0 +1,230 @@
+// Residual addition and RMS norm (moe_add_rmsnorm, moe_add_rmsnorm_q8):
+//   h = bf16(x + r)          (h = x without a residual)
+//   u = h / sqrt(mean(h^2) + eps) * g
+// and u either rounded once to bf16 or as 8-bit codes with one fp32 scale per
+// 32 values.  A row is read once and stays in registers between the sum of
+// squares and the outputs.
+#include <float.h>
+#include <math.h>
+
+#include "device_common.cuh"
+#include "op_common.cuh"
+#include "profile.cuh"
+
+namespace moe {
+namespace {
+
+using namespace dev;
+using namespace op;
+
+constexpr int kNormMaxHidden = 32768;
+constexpr float kQ8Smallest = 1e-30f;  // blocks below it are written as zeros
+
+struct NormParams {
+  const uint16_t* x;   // [T][H] bf16
+  const uint16_t* r;   // [T][H] bf16 or null
+  const float* g;      // [H] or null
+  uint16_t* h;         // [T][H] bf16 or null
+  uint16_t* u;         // [T][H] bf16 (bf16 output)
+  int8_t* q;           // [T][H] (8-bit output)
+  float* s;            // [T][H/32] (8-bit output)
+  int T, H;
+  float eps, inv_h;
+};
+
+// Sum over the threads of a row: a warp, or the CTA (`red`: one float per warp).
+template <bool kWarpRow>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = warp_sum(v);
+  if (kWarpRow) return v;
+  __syncthreads();  // red may still be read from an earlier call
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const int nw = blockDim.x >> 5;
+  return warp_sum((threadIdx.x & 31) < nw ? red[threadIdx.x & 31] : 0.0f);
+}
+
+// One row per CTA, or per warp (kWarpRow).  Each thread holds V vectors of 8
+// values, vector j at 8 * (j * threads + thread): a warp's 16-byte accesses
+// are contiguous, and the 32 values of a scale block sit in four
+// neighbouring lanes.
+template <int V, bool kWarpRow, bool kQ8>
+__global__ void __launch_bounds__(kWarpRow ? 256 : 1024) norm_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float red[32];
+  const int nthr = kWarpRow ? 32 : blockDim.x;
+  const int tid = kWarpRow ? (threadIdx.x & 31) : threadIdx.x;
+  const int row = kWarpRow ? blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+  dep_wait();
+  dep_release();
+  if (row >= p.T) return;  // whole warps (kWarpRow); never with one row per CTA
+  const size_t base = (size_t)row * p.H;
+  const int nvec = p.H >> 3;
+
+  uint4 xv[V], rv[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int v = j * nthr + tid;
+    xv[j] = rv[j] = make_uint4(0u, 0u, 0u, 0u);
+    if (v < nvec) {
+      xv[j] = *reinterpret_cast<const uint4*>(p.x + base + 8 * v);
+      if (p.r) rv[j] = *reinterpret_cast<const uint4*>(p.r + base + 8 * v);
+    }
+  }
+  float sum = 0.0f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    uint32_t* a = reinterpret_cast<uint32_t*>(&xv[j]);
+    const uint32_t* b = reinterpret_cast<const uint32_t*>(&rv[j]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // the statistics and u are those of the rounded h that the caller gets
+      if (p.r) a[i] = pack_bf16(bf_lo(a[i]) + bf_lo(b[i]), bf_hi(a[i]) + bf_hi(b[i]));
+      sum = fmaf(bf_lo(a[i]), bf_lo(a[i]), sum);
+      sum = fmaf(bf_hi(a[i]), bf_hi(a[i]), sum);
+    }
+  }
+  sum = row_sum<kWarpRow>(sum, red);
+  float inv = rsqrtf(sum * p.inv_h + p.eps);
+  if (isinf(sum)) {
+    // squares past the fp32 range (|h| above 1.8e19): the same with h scaled
+    // by 2^-70; an infinite h still gives inv = 0
+    float s2 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const uint32_t* a = reinterpret_cast<const uint32_t*>(&xv[j]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float lo = bf_lo(a[i]) * 0x1p-70f, hi = bf_hi(a[i]) * 0x1p-70f;
+        s2 = fmaf(lo, lo, s2);
+        s2 = fmaf(hi, hi, s2);
+      }
+    }
+    s2 = row_sum<kWarpRow>(s2, red);
+    inv = rsqrtf(s2 * p.inv_h) * 0x1p-70f;
+  }
+
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int v = j * nthr + tid;
+    const bool in = v < nvec;
+    const uint32_t* a = reinterpret_cast<const uint32_t*>(&xv[j]);
+    float u[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      u[2 * i] = bf_lo(a[i]) * inv;
+      u[2 * i + 1] = bf_hi(a[i]) * inv;
+    }
+    if (p.g && in) {
+      const float4 g0 = *reinterpret_cast<const float4*>(p.g + 8 * v);
+      const float4 g1 = *reinterpret_cast<const float4*>(p.g + 8 * v + 4);
+      u[0] *= g0.x, u[1] *= g0.y, u[2] *= g0.z, u[3] *= g0.w;
+      u[4] *= g1.x, u[5] *= g1.y, u[6] *= g1.z, u[7] *= g1.w;
+    }
+    if (p.h && in) *reinterpret_cast<uint4*>(p.h + base + 8 * v) = xv[j];
+    if constexpr (!kQ8) {
+      if (in)
+        *reinterpret_cast<uint4*>(p.u + base + 8 * v) =
+            make_uint4(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]), pack_bf16(u[4], u[5]), pack_bf16(u[6], u[7]));
+    } else {
+      // the largest magnitude as bits: infinities and NaN order above every
+      // finite value, so one maximum also says whether the block is finite
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(u[i]) & 0x7fffffffu);
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const float top = __uint_as_float(m);
+      float scale = top / 127.0f, to_q = 127.0f / top;
+      if (!(top >= kQ8Smallest)) scale = to_q = 0.0f;
+      if (m >= 0x7f800000u) scale = __uint_as_float(0x7fffffffu), to_q = 0.0f;
+      uint32_t w[2] = {0u, 0u};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = (to_q == 0.0f) ? 0 : __float2int_rn(u[i] * to_q);  // |u * 127 / top| rounds to 127 at most
+        w[i >> 2] |= (uint32_t)(c & 0xff) << (8 * (i & 3));
+      }
+      if (in) {
+        *reinterpret_cast<uint2*>(p.q + base + 8 * v) = make_uint2(w[0], w[1]);
+        if ((v & 3) == 0) p.s[(base >> 5) + (v >> 2)] = scale;
+      }
+    }
+  }
+}
+
+template <bool kQ8>
+cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
+  prof::Scope scope(kQ8 ? "add_rmsnorm_q8" : "add_rmsnorm", s);
+  const int nvec = p.H / 8;
+  if (nvec <= 1024) {
+    const int thr = (nvec + 31) / 32 * 32;
+    return launch_overlapped(norm_kernel<1, false, kQ8>, dim3(p.T), dim3(thr), 0, s, p);
+  }
+  const int thr = ((nvec + 3) / 4 + 31) / 32 * 32;
+  return launch_overlapped(norm_kernel<4, false, kQ8>, dim3(p.T), dim3(thr), 0, s, p);
+}
+
+moe_status add_rmsnorm(const void* x, const void* r, const float* g, float eps, int T, int H, void* h, void* u,
+                       int8_t* q, float* sc, bool q8, void* stream) {
+  if (T < 1 || T > 65536) return fail(MOE_ERR_CAPACITY, "n_tokens=%d outside [1, 65536]", T);
+  if (H < 32 || H > kNormMaxHidden || H % 32)
+    return fail(MOE_ERR_INVALID, "hidden=%d: a multiple of 32 in [32, %d] is needed", H, kNormMaxHidden);
+  if (!(eps >= 0.0f) || isinf(eps)) return fail(MOE_ERR_INVALID, "eps must be finite and not negative");
+  const size_t n = (size_t)T * H;
+  Buf in[3] = {{"x", x, 2 * n, 16}, {"residual", r, 2 * n, 16}, {"gain", g, 4 * (size_t)H, 16}};
+  Buf out[3] = {{"h", h, 2 * n, 16},
+                {q8 ? "u_q8" : "u", q8 ? (const void*)q : u, q8 ? n : 2 * n, 16},
+                {"u_scale", sc, n / 8, 4}};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  moe_status st;
+  for (int i = 0; i < 3; ++i)
+    if ((i == 0 || in[i].p) && (st = check_buf(in[i], dev)) != MOE_OK) return st;
+  for (int i = 0; i < (q8 ? 3 : 2); ++i)
+    if ((i != 0 || out[i].p) && (st = check_buf(out[i], dev)) != MOE_OK) return st;
+  // h and a bf16 u may be x or the residual itself (every thread reads its
+  // values of a row before it writes them); any other overlap is refused
+  for (int o = 0; o < 3; ++o) {
+    for (int i = 0; i < 3; ++i) {
+      const bool same = i < 2 && out[o].p == in[i].p && (o == 0 || (o == 1 && !q8));
+      if (overlap(out[o], in[i]) && !same)
+        return fail(MOE_ERR_INVALID, "%s overlaps %s", out[o].name, in[i].name);
+    }
+    for (int i = 0; i < o; ++i)
+      if (overlap(out[o], out[i])) return fail(MOE_ERR_INVALID, "%s overlaps %s", out[o].name, out[i].name);
+  }
+  NormParams p;
+  p.x = static_cast<const uint16_t*>(x);
+  p.r = static_cast<const uint16_t*>(r);
+  p.g = g;
+  p.h = static_cast<uint16_t*>(h);
+  p.u = static_cast<uint16_t*>(u);
+  p.q = q;
+  p.s = sc;
+  p.T = T;
+  p.H = H;
+  p.eps = eps;
+  p.inv_h = 1.0f / (float)H;
+  e = q8 ? launch_norm<true>(p, (cudaStream_t)stream) : launch_norm<false>(p, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "norm launch");
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" {
+
+moe_status moe_add_rmsnorm(const void* x_bf16, const void* residual_bf16, const float* gain, float eps, int n_tokens,
+                           int hidden, void* h_bf16, void* u_bf16, void* stream) {
+  return moe::add_rmsnorm(x_bf16, residual_bf16, gain, eps, n_tokens, hidden, h_bf16, u_bf16, nullptr, nullptr, false,
+                          stream);
+}
+
+moe_status moe_add_rmsnorm_q8(const void* x_bf16, const void* residual_bf16, const float* gain, float eps,
+                              int n_tokens, int hidden, void* h_bf16, int8_t* u_q8, float* u_scale, void* stream) {
+  return moe::add_rmsnorm(x_bf16, residual_bf16, gain, eps, n_tokens, hidden, h_bf16, nullptr, u_q8, u_scale, true,
+                          stream);
+}
+
+}  // extern "C"

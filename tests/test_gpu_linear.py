@@ -1,0 +1,187 @@
+"""moe_linear against the product in 64 bits (bounds: operators_ref.product_bound)."""
+import pytest
+import torch
+
+import quantized_expert_ffn_softmax_gb300 as moe
+import operators_ref as R
+
+pytestmark = pytest.mark.gpu
+
+# above 32 tokens each weight is rounded once to bf16, half a step at most
+GEMM_WEIGHT_ROUNDING = 2.0 ** -8
+
+
+def make(N, K, T, bias, device, seed=0):
+    q, s, w = R.quantized(seed + N + K, N, K)
+    b = 0.3 * torch.randn(N, generator=torch.Generator().manual_seed(seed + 5)) if bias else None
+    lin = moe.MoELinear(dict(in_features=K, out_features=N, max_tokens=T), dict(q=q, s=s, bias=b), False)
+    return lin, w, b
+
+
+def acts(T, K, seed=0):
+    g = torch.Generator().manual_seed(1000 + seed + T * 17 + K)
+    return (torch.randn(T, K, generator=g) * torch.exp(torch.randn(T, 1, generator=g))).bfloat16()
+
+
+def check(y, x64, w64, bias, rounding=0.0):
+    y64 = R.product(x64, w64, bias)
+    off = (y.double().cpu() - y64).abs()
+    bound = R.product_bound(x64, w64, y64, bias, rounding)
+    assert (off <= bound).all(), (off / bound).max().item()
+
+
+SMALL = [(1, 16, 32), (1, 1, 32), (1, 17, 64), (1, 2048, 2048), (2, 100, 96), (3, 2049, 160), (4, 33, 8192), (5, 640, 1056),
+         (8, 257, 2080), (9, 1000, 256), (16, 4099, 512), (17, 48, 2048), (31, 515, 1024), (32, 1024, 4096),
+         (1, 40000, 256), (8, 5000, 4128), (32, 16, 32768), (24, 9000, 128)]
+
+
+@pytest.mark.parametrize("T,N,K", SMALL)
+@pytest.mark.parametrize("bias", [False, True])
+def test_small_batches(cuda_device, T, N, K, bias):
+    lin, w, b = make(N, K, T, bias, cuda_device)
+    x = acts(T, K)
+    y = lin.forward(x.to(cuda_device))
+    check(y, x.double(), w, b)
+    assert moe.moe_linear_status_sync(lin.handle) == moe.MOE_OK
+
+
+@pytest.mark.parametrize("T,N,K", SMALL)
+def test_small_batches_q8(cuda_device, T, N, K):
+    lin, w, b = make(N, K, T, True, cuda_device)
+    g = torch.Generator().manual_seed(T + N + K)
+    q = torch.randint(-127, 128, (T, K), generator=g).to(torch.int8)
+    s = torch.rand(T, K // 32, generator=g) + 0.01
+    y = lin.forward_q8(q.to(cuda_device), s.to(cuda_device))
+    check(y, R.q8_values(q, s), w, b)
+
+
+LARGE = [(33, 100, 64), (40, 2048, 2048), (64, 300, 96), (65, 1, 32), (100, 4111, 2080), (128, 128, 128),
+         (129, 513, 1056), (200, 777, 4096), (256, 256, 256), (257, 1025, 544), (511, 48, 8192), (700, 2560, 2048),
+         (1025, 640, 160), (2050, 2050, 320), (65, 20000, 64), (40, 70000, 32)]
+
+
+@pytest.mark.parametrize("T,N,K", LARGE)
+@pytest.mark.parametrize("bias", [False, True])
+def test_large_batches(cuda_device, T, N, K, bias):
+    lin, w, b = make(N, K, T, bias, cuda_device)
+    x = acts(T, K)
+    y = lin.forward(x.to(cuda_device))
+    check(y, x.double(), w, b, GEMM_WEIGHT_ROUNDING)
+    assert moe.moe_linear_status_sync(lin.handle) == moe.MOE_OK
+
+
+@pytest.mark.parametrize("T", [1, 5, 32, 33, 300])
+def test_device_and_host_weights_agree(cuda_device, T):
+    N, K = 1030, 608
+    q, s, _ = R.quantized(3, N, K)
+    b = torch.randn(N)
+    cfg = dict(in_features=K, out_features=N, max_tokens=T)
+    a = moe.MoELinear(cfg, dict(q=q, s=s, bias=b), False)
+    qd, sd, bd = q.to(cuda_device), s.to(cuda_device), b.to(cuda_device)
+    d = moe.MoELinear(cfg, dict(q=qd, s=sd, bias=bd), True)
+    qd.zero_(), sd.zero_(), bd.zero_()  # the handle keeps its own copy
+    x = acts(T, K).to(cuda_device)
+    assert torch.equal(a.forward(x), d.forward(x))
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 3000, 2048), (4, 8192, 2048), (32, 515, 4096), (200, 4111, 2080), (1100, 1030, 544)])
+def test_repeats_are_bit_identical_and_guards_stay(cuda_device, T, N, K):
+    lin, _, _ = make(N, K, T, True, cuda_device)
+    x = acts(T, K).to(cuda_device)
+    first = lin.forward(x)
+    y = torch.full(((T + 1) * N + 8,), 7.0, dtype=torch.bfloat16, device=cuda_device)
+    for _ in range(20):
+        moe.moe_linear_forward(lin.handle, x, T, y[:T * N])
+        assert torch.equal(y[:T * N].view(T, N), first)
+    assert (y[T * N:] == 7).all()
+    # an output that starts 2 bytes past a 16-byte boundary
+    z = torch.full((T * N + 9,), 7.0, dtype=torch.bfloat16, device=cuda_device)
+    moe.moe_linear_forward(lin.handle, x, T, z[1:1 + T * N])
+    assert torch.equal(z[1:1 + T * N].view(T, N), first) and z[0] == 7 and (z[1 + T * N:] == 7).all()
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 600, 2048), (8, 600, 96), (20, 600, 544), (300, 600, 544)])
+def test_non_finite_tokens_stay_apart(cuda_device, T, N, K):
+    lin, w, b = make(N, K, T, True, cuda_device)
+    x = acts(T, K)
+    bad = [t for t in (0, T // 2, T - 1)][:max(1, min(3, T))]
+    x[0, 3] = float("inf")
+    x[T // 2, K - 1] = float("nan")
+    x[T - 1, K // 2] = float("-inf")
+    y = lin.forward(x.to(cuda_device)).cpu()
+    assert not torch.isfinite(y[sorted(set(bad))]).any()
+    rest = [t for t in range(T) if t not in bad]
+    if rest:
+        check(y[rest], x[rest].double(), w, b, 0.0 if T <= 32 else GEMM_WEIGHT_ROUNDING)
+
+
+@pytest.mark.parametrize("T", [1, 33, 600])
+def test_extreme_scales(cuda_device, T):
+    """Scales from the smallest subnormal to the largest fp16 value, zeros, every code."""
+    N, K = 64, 256
+    g = torch.Generator().manual_seed(9)
+    q = torch.randint(0, 256, (N, K // 2), generator=g).to(torch.uint8)
+    s = torch.exp2(torch.randint(-24, 16, (N, K // 32), generator=g).float()).half()
+    s[0] = 0
+    s[1] = 65504.0
+    s[2] = 6e-8
+    lin = moe.MoELinear(dict(in_features=K, out_features=N, max_tokens=T), dict(q=q, s=s), False)
+    c = torch.stack((q & 15, q >> 4), -1).view(N, K // 32, 32).double() - 8
+    w = (c * s.double()[..., None]).view(N, K)
+    x = acts(T, K)
+    check(lin.forward(x.to(cuda_device)), x.double(), w, None, 0.0 if T <= 32 else GEMM_WEIGHT_ROUNDING)
+
+
+def test_refusals(cuda_device):
+    N, K, T = 64, 128, 40
+    lin, _, _ = make(N, K, T, False, cuda_device)
+    x = acts(T, K).to(cuda_device)
+    y = torch.empty(T, N, dtype=torch.bfloat16, device=cuda_device)
+    big = torch.empty(T * K + 8, dtype=torch.bfloat16, device=cuda_device)
+    for args, status in (((x, 0, y), moe.MOE_ERR_CAPACITY), ((x, T + 1, y), moe.MOE_ERR_CAPACITY),
+                         ((None, T, y), moe.MOE_ERR_INVALID), ((x, T, None), moe.MOE_ERR_INVALID),
+                         ((x.cpu(), T, y), moe.MOE_ERR_INVALID), ((x, T, y.cpu()), moe.MOE_ERR_INVALID),
+                         ((big[1:1 + T * K], T, y), moe.MOE_ERR_INVALID), ((x, T, x), moe.MOE_ERR_INVALID)):
+        with pytest.raises(moe.MoeError) as ei:
+            moe.moe_linear_forward(lin.handle, *args)
+        assert ei.value.status == status
+    q = torch.zeros(T, K, dtype=torch.int8, device=cuda_device)
+    s = torch.zeros(T, K // 32, device=cuda_device)
+    with pytest.raises(moe.MoeError) as ei:  # the 8-bit form is for decode batches
+        moe.moe_linear_forward_q8(lin.handle, q, s, 33, y)
+    assert ei.value.status == moe.MOE_ERR_CAPACITY
+    for args in ((None, s, 4, y), (q, None, 4, y), (q, s, 4, None), (q.cpu(), s, 4, y), (q, s, 4, q)):
+        with pytest.raises(moe.MoeError) as ei:
+            moe.moe_linear_forward_q8(lin.handle, *args)
+        assert ei.value.status == moe.MOE_ERR_INVALID
+    with pytest.raises(ValueError):
+        lin.forward(x.float())
+    with pytest.raises(ValueError):
+        lin.forward(x[:, :64])
+    with pytest.raises(ValueError):
+        lin.forward_q8(q, s[:3])
+
+
+@pytest.mark.parametrize("T", [1, 4, 32, 200])
+def test_side_stream_and_graph(cuda_device, T):
+    N, K = 1536, 2048
+    lin, _, _ = make(N, K, T, True, cuda_device)
+    back, _, _ = make(K, N, T, False, cuda_device, seed=1)
+    x = acts(T, K).to(cuda_device)
+    y0 = lin.forward(x)
+    z0 = back.forward(y0)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    y = torch.zeros_like(y0)
+    moe.moe_linear_forward(lin.handle, x, T, y, st)
+    st.synchronize()
+    assert torch.equal(y, y0)
+    x1, z = x.clone(), torch.zeros_like(z0)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe.moe_linear_forward(lin.handle, x1, T, y)
+        moe.moe_linear_forward(back.handle, y, T, z)
+    for k in range(3):
+        x1.copy_(x if k != 1 else -x)
+        g.replay()
+        assert torch.equal(z, z0 if k != 1 else back.forward(lin.forward(-x)))
