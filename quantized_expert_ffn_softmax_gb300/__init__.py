@@ -145,16 +145,33 @@ def _ptr(a) -> Optional[int]:
     raise TypeError("cannot take the address of %r" % type(a))
 
 
-def _stream(stream) -> Optional[int]:
-    if stream is None:
+_current = None  # () -> handle of torch's current stream, once CUDA is known to be available
+
+
+def _current_stream() -> Optional[int]:
+    # torch.cuda.current_stream() builds a Stream object: 2.9 us a call on a
+    # Grace core, against 0.2 us for the raw handle (a decode-sized kernel
+    # takes 1.5 us)
+    global _current
+    if _current is None:
         try:
             import torch
-
-            if torch.cuda.is_available():
-                return torch.cuda.current_stream().cuda_stream
         except ImportError:
-            pass
-        return None
+            return None
+        if not torch.cuda.is_available():
+            return None
+        torch.cuda.init()
+        device, raw = (getattr(torch._C, n, None) for n in ("_cuda_getDevice",
+                                                            "_cuda_getCurrentRawStream"))
+        if device is None or raw is None:
+            return torch.cuda.current_stream().cuda_stream
+        _current = lambda: raw(device())
+    return _current()
+
+
+def _stream(stream) -> Optional[int]:
+    if stream is None:
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
