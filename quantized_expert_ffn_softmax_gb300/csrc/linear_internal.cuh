@@ -15,28 +15,51 @@ namespace lin {
 //   1024 B of codes: two halves of 64 inputs (two scale blocks each); in a
 //     half lane l = 4 g + t of a warp finds 16 bytes at 16 l: one word of
 //     block 0 row g, block 0 row g + 8, block 1 row g, block 1 row g + 8.
-//     A word holds the inputs 8 t .. 8 t + 7 of its block: input 2 i in
-//     nibble i and input 2 i + 1 in nibble i + 4, so that
-//     (word >> 4 i) & 0x000f000f is the pair (2 i, 2 i + 1).
+//     A word holds the inputs 8 t .. 8 t + 7 of its block, inputs 2 i and
+//     2 i + 1 as a pair that a rotation by 4 i brings to bits 3-6 and 19-22
+//     (word_of below).
 //   128 B of scales: at 16 g the four block scales of row g, then of row
-//     g + 8.
-// The words are the A fragments of mma.m16n8k16 as they stand (two MMAs per
-// scale block), and eight consecutive inputs of a row in one 16-byte store
-// of the tcgen05 path's shared-memory tiles.  Rows past N and inputs past K
-// have scale 0.
+//     g + 8, each times the power of two that brings the largest magnitude of
+//     its row to [2^15, 2^16) (exact: that only shifts exponents up); row_f
+//     is the inverse.
+// The words are the A fragments of mma.m16n8k16 (two MMAs per scale block),
+// and eight consecutive inputs of a row in one 16-byte store of the tcgen05
+// path's shared-memory tiles.  Rows past N and inputs past K have scale 0.
+__host__ __device__ constexpr uint32_t word_of(const uint32_t (&c)[8]) {
+  uint32_t w = 0;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t pair = c[2 * i] << 3 | c[2 * i + 1] << 19;
+    w |= i ? (pair << (4 * i) | pair >> (32 - 4 * i)) : pair;
+  }
+  return w;
+}
+
 constexpr int kTileRows = 16;
 constexpr int kTileK = 128;
 constexpr int kTileCodes = 1024;
 constexpr int kTileBytes = 1152;
-constexpr int kMaxQ8Tokens = 32;
+constexpr int kSmallTokens = 32;  // largest batch of the small-batch kernel
 
 struct Weights {
   const uint8_t* tiles;
-  const float* bias;  // [N] or null
+  const float* row_f;  // [N] scale = stored scale * row_f
+  const float* bias;   // [N] or null
   int K, N;
   int kc;             // tiles along K
   int nt;             // tiles along N
 };
+
+// linear_gemm.cu: batches above kSmallTokens.
+// x as fp16, every token scaled by a power of two to a largest magnitude in
+// [1, 2): rows of x16 and the inverse factors.
+struct XIn {
+  const uint16_t* x;  // [T][K] bf16, or
+  const int8_t* q;    // [T][K] codes and
+  const float* qs;    // [T][K/32] scales
+};
+size_t gemm_workspace(int K, int max_tokens);
+moe_status gemm_init(moe_linear* L, void* ws);
+moe_status launch_gemm(moe_linear* L, const XIn& in, int T, uint16_t* y, cudaStream_t s);
 
 }  // namespace lin
 }  // namespace moe
@@ -46,6 +69,9 @@ struct moe_linear {
   moe::lin::Weights w;
   void* block = nullptr;
   int* err = nullptr;
+  void* x16 = nullptr;      // [max_tokens][K] fp16 operand rows (batches above kSmallTokens)
+  float* x_f = nullptr;     // [max_tokens] token factors
+  CUtensorMap xmap[16];     // x16 with boxes of 64 inputs by 16 (i + 1) tokens
   int device = 0;
   int num_sms = 0;
 };
