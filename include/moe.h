@@ -288,7 +288,7 @@ moe_status moe_add_rmsnorm_q8(const void* x_bf16, const void* residual_bf16, con
 typedef struct moe_linear moe_linear; /* opaque, owned by the library */
 
 /* Limits: 32 <= in_features <= 32768, a multiple of 32; 1 <= out_features <=
- * 1048576; 1 <= max_tokens <= 65536 (above 32 the handle also holds a
+ * 1048576; 1 <= max_tokens <= 65536 (above 8 the handle also holds a
  * workspace of about 2 * max_tokens * in_features bytes). */
 typedef struct {
   int32_t in_features;  /* K */
@@ -315,10 +315,13 @@ void moe_linear_destroy(moe_linear* linear);
 
 /* y = x W^T + bias: x bf16 [n_tokens][K], y bf16 [n_tokens][N], results
  * bit-identical from call to call.  Calls on one handle must not overlap on
- * the GPU (they share its workspace).  Up to 32 tokens no weight and no x is
- * rounded; above that both are rounded to fp16 operands, each token and each
- * row of W scaled by a power of two.  A token with an infinity or NaN in x has
- * unspecified non-finite values in y; other tokens are not affected. */
+ * the GPU (they share its workspace).  Sums are fp32, the weights exact up to
+ * 8 tokens; one or two bf16 tokens may be taken as integers per block of 32
+ * inputs (off by at most 2^-14 of the block's largest |x|, exact down to 1/64
+ * of it), and above 8 tokens x and W may be rounded to fp16 operands, each
+ * token and each row of W scaled by a power of two.  A token with an infinity
+ * or NaN in x has unspecified non-finite values in y; other tokens are not
+ * affected. */
 moe_status moe_linear_forward(moe_linear* linear, const void* x_bf16, int n_tokens, void* y_bf16,
                               void* stream);
 

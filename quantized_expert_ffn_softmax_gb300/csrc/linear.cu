@@ -1,17 +1,21 @@
 // Projections with 4-bit weights (moe_linear): y = x W^T + b, W in the
 // experts' format (codes with one binary16 scale per 32 inputs).
 //
-// Batches of up to 32 tokens, in bf16 or in 8 bits with scales: the work is
-// reading W once (0.5625 bytes per weight), so the weights go straight from
-// HBM into registers and are multiplied there with the legacy tensor path
-// (mma.sync): W is the 16-row operand A, unpacked exactly to bf16 integers
-// (code - 8), up to four 8-token column tiles are operand B, and the fp32
-// result of every 32-input block is multiplied by the block's scale.  No
-// weight and no activation is rounded.
+// Small batches read W once (0.5625 bytes per weight), so the weights go
+// straight from HBM through a ring in shared memory into registers; what
+// bounds these kernels is the number of instructions per weight, first of all
+// the unpacking on the integer pipe.
+//   dot_kernel    1 or 2 tokens in bf16, up to 4 in 8 bits: integer dot
+//                 products (dp4a) of the codes with x as integers
+//   small_kernel  up to 16 tokens: the legacy tensor path (mma.sync), W the
+//                 16-row operand A unpacked exactly to bf16 integers, up to two
+//                 8-token column tiles operand B
+// In both the result of every 32-input block is multiplied by its scale in
+// fp32.  Larger batches: linear_gemm.cu.
 #include <math.h>
-#include <stdlib.h>
 
 #include <new>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "linear_internal.cuh"
@@ -54,18 +58,19 @@ __global__ void pack_kernel(const uint8_t* __restrict__ q, const uint16_t* __res
   for (int half = 0; half < 2; ++half) {
     uint32_t w[4];
     for (int i = 0; i < 4; ++i) {
-      const int row = row0 + g + 8 * (i & 1), k = k0 + 64 * half + 32 * (i >> 1) + 8 * t;
-      uint32_t c[8] = {8, 8, 8, 8, 8, 8, 8, 8};  // weight 0
+      const int row = row0 + frag_row(g) + 8 * (i & 1), k = k0 + 64 * half + 32 * (i >> 1) + 8 * t;
+      uint32_t v = 0x88888888u;  // code 8: weight 0
       if (row < N && k < K) {
         const uint8_t* b = q + (size_t)row * (K / 2) + k / 2;  // four bytes: inputs k .. k + 7
-        for (int j = 0; j < 4; ++j) c[2 * j] = b[j] & 15, c[2 * j + 1] = b[j] >> 4;
+        v = 0;
+        for (int j = 0; j < 4; ++j) v |= (uint32_t)(b[j] & 15) << (4 * j) | (uint32_t)(b[j] >> 4) << (4 * j + 16);
       }
-      w[i] = word_of(c);
+      w[i] = v;
     }
     *reinterpret_cast<uint4*>(dst + 512 * half + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  for (int i = lane; i < 64; i += 32) {  // scale i: 8 g' + (0..3 row g', 4..7 row g' + 8)
-    const int row = row0 + (i >> 3) + 8 * ((i >> 2) & 1), blk = k0 / 32 + (i & 3);
+  for (int i = lane; i < 64; i += 32) {  // scale i: fragment row i / 8, then block
+    const int row = row0 + frag_row(i >> 3) + 8 * ((i >> 2) & 1), blk = k0 / 32 + (i & 3);
     uint16_t v = 0;
     if (row < N && blk < K / 32)
       v = __half_as_ushort(__float2half_rn(__half2float(__ushort_as_half(s[(size_t)row * (K / 32) + blk])) / row_f[row]));
@@ -91,18 +96,16 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-// Pair i of a word as bf16 integers code - 8: a 4-bit code ORed into bits 3-6
-// of 16.0 reads 16 + code, and the difference to 24 is exact.  (Taking the
-// offset off in the accumulator instead, with an MMA of constant -24 for
+// Pair i of a word as bf16 integers code - 8: a 4-bit code ORed into the
+// mantissa of 128.0 reads 128 + code, and the difference to 136 is exact.
+// (Taking the offset off in the accumulator instead, with an MMA of a constant
 // operand A, saves 8 instructions per lane and block but is slower: these
 // kernels wait for the legacy MMA pipe first.)
 __device__ __forceinline__ uint32_t unpack_pair(uint32_t w, int i) {
   uint32_t v;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
-      : "=r"(v)
-      : "r"(i == 3 ? __funnelshift_r(w, w, 12) : w >> (4 * i)), "r"(0x00780078u), "r"(0x41804180u));
-  const __nv_bfloat162 k24 = __halves2bfloat162(__ushort_as_bfloat16(0x41C0), __ushort_as_bfloat16(0x41C0));
-  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), k24);
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w >> (4 * i)), "r"(0x000f000fu), "r"(0x43004300u));
+  const __nv_bfloat162 k136 = __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));
+  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), k136);
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
@@ -139,43 +142,53 @@ struct XBlock<NT, true> {
 // contiguous part of the K tiles each (their partial sums meet in shared
 // memory, in one fixed order).  A warp streams its weights through a ring of
 // its own of ST stages in shared memory (16-byte asynchronous copies, no
-// barrier between warps); x comes through L1.
-template <int NT, int MT, int ST, int kCtas, bool kQ8>
-__global__ void __launch_bounds__(256, kCtas) small_kernel(const __grid_constant__ SmallParams p, int S) {
-  extern __shared__ __align__(128) unsigned char smem[];
-  constexpr int kStage = MT * kTileBytes;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  unsigned char* ring = smem + warp * ST * kStage;
-  float* part = reinterpret_cast<float*>(smem + 8 * ST * kStage);
-  const int kc = p.w.kc, K = p.w.K;
-  const int ks = warp % S, grp = warp / S;
-  const int c0 = ks * kc / S, c1 = (ks + 1) * kc / S;
-  const int units = (p.w.nt + MT - 1) / MT;
-  const int ustep = gridDim.x * (8 / S);
-  const int unit0 = blockIdx.x * (8 / S) + grp;
+// barrier between warps).
+template <int MT, int ST>
+struct Stream {
+  static constexpr int kStage = MT * kTileBytes;
+  static constexpr int kBytes = 8 * ST * kStage;  // rings of a CTA
+  const Weights& w;
+  int units, ustep, grp, ks, unit0, c0, c1;  // of this warp
+  const unsigned char* ring;
+  int slot = 0;
+  // next stage to fill: unit, K tile, this lane's source and destination
+  int lu, lc;
+  const uint8_t* lsrc;
+  uint32_t ldst, lend, mstep[MT];
 
-  // Next stage to fill: unit, K tile, this lane's source and destination.
-  // Tiles of a unit past the end are the last tile again (not stored).
-  int lu = unit0, lc = c0;
-  const uint8_t* lsrc = p.w.tiles;
-  uint32_t ldst = smem_u32(ring) + 16 * lane;
-  const uint32_t lend = ldst + ST * kStage;
-  uint32_t mstep[MT];
-  auto source = [&]() {
-    const int tile = min(lu * MT, p.w.nt - 1);
-    lsrc = p.w.tiles + ((size_t)tile * kc + c0) * kTileBytes + 16 * lane;
+  __device__ __forceinline__ Stream(const Weights& w_, int S, unsigned char* smem) : w(w_) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grp = warp / S;
+    ks = warp % S;
+    units = (w.nt + MT - 1) / MT;
+    ustep = gridDim.x * (8 / S);
+    unit0 = blockIdx.x * (8 / S) + grp;
+    c0 = ks * w.kc / S;
+    c1 = (ks + 1) * w.kc / S;
+    ring = smem + warp * ST * kStage;
+    lu = unit0;
+    lc = c0;
+    ldst = smem_u32(ring) + 16 * lane;
+    lend = ldst + ST * kStage;
+    source();
 #pragma unroll
-    for (int m = 0; m < MT; ++m) mstep[m] = (uint32_t)(min(m, p.w.nt - 1 - tile) * kc * kTileBytes);
-  };
-  source();
-  auto issue = [&]() {
+    for (int i = 0; i < ST - 1; ++i) issue();
+  }
+  // Tiles of a unit past the end are the last tile again (not stored).
+  __device__ __forceinline__ void source() {
+    const int tile = min(lu * MT, w.nt - 1);
+    lsrc = w.tiles + ((size_t)tile * w.kc + c0) * kTileBytes + 16 * (threadIdx.x & 31);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) mstep[m] = (uint32_t)(min(m, w.nt - 1 - tile) * w.kc * kTileBytes);
+  }
+  __device__ __forceinline__ void issue() {
     if (lu < units) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const uint8_t* src = lsrc + mstep[m];
         cp_async_16(ldst + m * kTileBytes, src);
         cp_async_16(ldst + m * kTileBytes + 512, src + 512);
-        if (lane < 8) cp_async_16(ldst + m * kTileBytes + kTileCodes, src + kTileCodes);
+        if ((threadIdx.x & 31) < 8) cp_async_16(ldst + m * kTileBytes + kTileCodes, src + kTileCodes);
       }
       lsrc += kTileBytes;
       if (++lc == c1) {
@@ -187,9 +200,201 @@ __global__ void __launch_bounds__(256, kCtas) small_kernel(const __grid_constant
     cp_async_commit();
     ldst += kStage;
     if (ldst == lend) ldst -= ST * kStage;
-  };
+  }
+  // The next stage: there for every lane, and every lane is done with the one
+  // before, whose slot is refilled.
+  __device__ __forceinline__ const unsigned char* next() {
+    cp_async_wait<ST - 2>();
+    __syncwarp();
+    issue();
+    const unsigned char* st = ring + slot * kStage;
+    slot = slot + 1 == ST ? 0 : slot + 1;
+    return st;
+  }
+};
+
+// ------------------------------------------------------------ dot products
+// x as integers, per block of 32: 8-bit x as it is; bf16 x as q * 2^(e - 13)
+// with 2^e <= max|x| < 2^(e + 1) over the block, so that every value down to
+// 1/64 of the block's largest is exact and smaller ones are off by 2^(e - 14)
+// at most; |q| <= 16320 = 256 hi + lo with hi and lo in 8 bits.
+// A lane holds eight inputs of two rows of a block per step: their dot product
+// with the codes is exact in 32 bits; the -8 of the codes and the bits that
+// make the integer a float (2^23 + 2^22 as an exponent) ride on the
+// accumulator's initial value.
+constexpr int kFloatBias = 0x4B400000;  // 12582912.0f
+template <int TT, int MT, int ST, int kCtas, bool kQ8>
+__global__ void __launch_bounds__(256, kCtas) dot_kernel(const __grid_constant__ SmallParams p, int S) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  using Planes = typename std::conditional<kQ8, uint2, uint4>::type;  // codes, or hi and lo
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, K = p.w.K;
+  Stream<MT, ST> in(p.w, S, smem);
+  const int nv = p.w.kc * (kTileK / 8);  // vectors of 8 inputs, past K zeros
+  Planes* planes = reinterpret_cast<Planes*>(smem + in.kBytes);
+  int2* meta = reinterpret_cast<int2*>(planes + TT * nv);  // scale of the block, initial value
+  float* part = reinterpret_cast<float*>(meta + TT * nv);
+  dep_wait();
+  dep_release();
+
+  for (int i0 = 0; i0 < TT * nv; i0 += 256) {  // (nv is a multiple of 4: blocks are four neighbouring lanes)
+    const int i = i0 + threadIdx.x, tok = i / nv, v = i - tok * nv;
+    const bool here = tok < min(p.T, TT) && 8 * v < K;
+    // inputs 2 j in the low, 2 j + 1 in the high nibbles' order of dp4a
+    constexpr int kPos[8] = {0, 4, 1, 5, 2, 6, 3, 7};
+    float scale;
+    int sum = 0;
+    uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+    if constexpr (kQ8) {
+      uint2 c = make_uint2(0u, 0u);
+      if (here) c = *reinterpret_cast<const uint2*>(p.q + (size_t)tok * K + 8 * v);
+      scale = here ? p.qs[(size_t)tok * (K >> 5) + (v >> 2)] : 0.0f;
+      hi[0] = __byte_perm(c.x, c.y, 0x5140), hi[1] = __byte_perm(c.x, c.y, 0x7362);
+      sum = __dp4a((int)c.x, 0x01010101, __dp4a((int)c.y, 0x01010101, 0));
+    } else {
+      uint4 c = make_uint4(0u, 0u, 0u, 0u);
+      if (here) c = *reinterpret_cast<const uint4*>(p.x + (size_t)tok * K + 8 * v);
+      const float f[8] = {bf_lo(c.x), bf_hi(c.x), bf_lo(c.y), bf_hi(c.y), bf_lo(c.z), bf_hi(c.z), bf_lo(c.w), bf_hi(c.w)};
+      uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < ST - 1; ++i) issue();  // the weights are the library's own: nothing to wait for
+      for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7fffffffu);
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const int e = max((int)(m >> 23) - 127, -113);
+      const bool finite = m < 0x7f800000u;  // else the block's scale makes every y of the token NaN
+      const float up = finite ? pow2f(13 - e) : 0.0f;
+      scale = finite ? pow2f(e - 13) : __uint_as_float(0x7fffffffu);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int qv = finite ? __float2int_rn(f[kPos[j]] * up) : 0;
+        const int h = (qv + 128) >> 8, l = qv - 256 * h;
+        sum += qv;
+        hi[j >> 2] |= (uint32_t)(h & 0xff) << (8 * (j & 3));
+        lo[j >> 2] |= (uint32_t)(l & 0xff) << (8 * (j & 3));
+      }
+    }
+    if (i >= TT * nv) continue;
+    if constexpr (kQ8)
+      planes[i] = make_uint2(hi[0], hi[1]);
+    else
+      planes[i] = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+    meta[i] = make_int2(__float_as_int(scale), kFloatBias - 8 * sum);
+  }
+  __syncthreads();
+
+  for (int unit = in.unit0; unit - in.grp < in.units; unit += in.ustep) {  // the same number of turns for every warp
+    float acc[MT][TT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int k = 0; k < TT; ++k) acc[m][k][0] = acc[m][k][1] = 0.0f;
+    if (unit < in.units) {
+      for (int c = in.c0; c < in.c1; ++c) {
+        const unsigned char* st = in.next();
+        uint4 sc[MT], wv[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          sc[m] = *reinterpret_cast<const uint4*>(st + m * kTileBytes + kTileCodes + 16 * g);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          Planes px[TT];
+          int2 mx[TT];
+#pragma unroll
+          for (int k = 0; k < TT; ++k) {
+            const int v = k * nv + c * (kTileK / 8) + 4 * b + t;
+            px[k] = planes[v];
+            mx[k] = meta[v];
+          }
+          if ((b & 1) == 0) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+              wv[m] = *reinterpret_cast<const uint4*>(st + m * kTileBytes + 512 * (b >> 1) + 16 * lane);
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const uint32_t s0 = (b >> 1) ? sc[m].y : sc[m].x, s1 = (b >> 1) ? sc[m].w : sc[m].z;
+            const __half2 h0 = *reinterpret_cast<const __half2*>(&s0), h1 = *reinterpret_cast<const __half2*>(&s1);
+            const float sr[2] = {(b & 1) ? __high2float(h0) : __low2float(h0),
+                                 (b & 1) ? __high2float(h1) : __low2float(h1)};
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const uint32_t w = (b & 1) ? (r ? wv[m].w : wv[m].z) : (r ? wv[m].y : wv[m].x);
+              const int we = (int)(w & 0x0f0f0f0fu), wo = (int)((w >> 4) & 0x0f0f0f0fu);
+#pragma unroll
+              for (int k = 0; k < TT; ++k) {
+                int d;
+                if constexpr (kQ8) {
+                  d = __dp4a(we, (int)px[k].x, __dp4a(wo, (int)px[k].y, mx[k].y));
+                } else {
+                  const int h = __dp4a(we, (int)px[k].x, __dp4a(wo, (int)px[k].y, 0));
+                  d = h * 256 + __dp4a(we, (int)px[k].z, __dp4a(wo, (int)px[k].w, mx[k].y));
+                }
+                const float v = __int_as_float(d) - __int_as_float(kFloatBias);
+                acc[m][k][r] = fmaf(v, sr[r] * __int_as_float(mx[k].x), acc[m][k][r]);
+              }
+            }
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int k = 0; k < TT; ++k)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          acc[m][k][r] += __shfl_xor_sync(0xffffffffu, acc[m][k][r], 1);
+          acc[m][k][r] += __shfl_xor_sync(0xffffffffu, acc[m][k][r], 2);
+        }
+    if (S > 1) {
+      const int warp = threadIdx.x >> 5;
+      __syncthreads();  // the sums of the unit before are read
+      if (t == 0) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int k = 0; k < TT; ++k)
+            *reinterpret_cast<float2*>(&part[((warp * MT + m) * TT + k) * 16 + 2 * g]) =
+                make_float2(acc[m][k][0], acc[m][k][1]);
+      }
+      __syncthreads();
+      if (in.ks == 0) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int k = 0; k < TT; ++k)
+            for (int i = 1; i < S; ++i) {
+              const float2 v = *reinterpret_cast<const float2*>(&part[(((warp + i) * MT + m) * TT + k) * 16 + 2 * g]);
+              acc[m][k][0] += v.x, acc[m][k][1] += v.y;
+            }
+      }
+    }
+    if (unit < in.units && in.ks == 0 && t == 0) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = (unit * MT + m) * kTileRows + frag_row(g) + 8 * r;
+          if (row < p.w.N) {
+            const float rf = __ldg(p.w.row_f + row), bias = p.w.bias ? __ldg(p.w.bias + row) : 0.0f;
+#pragma unroll
+            for (int k = 0; k < TT; ++k)
+              if (k < p.T)
+                p.y[(size_t)k * p.w.N + row] = __bfloat16_as_ushort(__float2bfloat16_rn(fmaf(acc[m][k][r], rf, bias)));
+          }
+        }
+    }
+  }
+  cp_async_wait<0>();  // (only empty groups are left)
+}
+
+// ------------------------------------------------------------ legacy MMA
+template <int NT, int MT, int ST, int kCtas, bool kQ8>
+__global__ void __launch_bounds__(256, kCtas) small_kernel(const __grid_constant__ SmallParams p, int S) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, K = p.w.K;
+  Stream<MT, ST> in(p.w, S, smem);  // the weights are the library's own: nothing to wait for
+  float* part = reinterpret_cast<float*>(smem + in.kBytes);
+  const int units = in.units, grp = in.grp, ks = in.ks, c0 = in.c0, c1 = in.c1;
   dep_wait();
   dep_release();
 
@@ -219,8 +424,7 @@ __global__ void __launch_bounds__(256, kCtas) small_kernel(const __grid_constant
   };
   load_x(xb[0], c0 * kTileK);
 
-  int slot = 0;
-  for (int unit = unit0; unit - grp < units; unit += ustep) {  // the same number of turns for every warp
+  for (int unit = in.unit0; unit - grp < units; unit += in.ustep) {  // the same number of turns for every warp
     float acc[MT][NT][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -230,11 +434,7 @@ __global__ void __launch_bounds__(256, kCtas) small_kernel(const __grid_constant
         for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
     if (unit < units) {
       for (int c = c0; c < c1; ++c) {
-        cp_async_wait<ST - 2>();
-        __syncwarp();  // the stage is there for every lane, and every lane is done with the one before
-        issue();
-        const unsigned char* st = ring + slot * kStage;
-        slot = slot + 1 == ST ? 0 : slot + 1;
+        const unsigned char* st = in.next();
         uint4 sc[MT], wv[MT];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -319,7 +519,7 @@ __global__ void __launch_bounds__(256, kCtas) small_kernel(const __grid_constant
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int row = (unit * MT + m) * kTileRows + g + 8 * h;
+          const int row = (unit * MT + m) * kTileRows + frag_row(g) + 8 * h;
           if (row < p.w.N) {
             const float rf = __ldg(p.w.row_f + row), bias = p.w.bias ? __ldg(p.w.bias + row) : 0.0f;
 #pragma unroll
@@ -338,47 +538,97 @@ __global__ void __launch_bounds__(256, kCtas) small_kernel(const __grid_constant
   cp_async_wait<0>();  // (only empty groups are left)
 }
 
-template <int NT, int MT, int ST, int kCtas, bool kQ8>
-cudaError_t launch_small_as(const SmallParams& p, int num_sms, cudaStream_t s) {
-  constexpr int kRing = 8 * ST * MT * kTileBytes, kPart = 8 * MT * NT * 512;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(small_kernel<NT, MT, ST, kCtas, kQ8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + kPart);
-  if (attr != cudaSuccess) return attr;
-  // Warps per unit: the smallest power of two whose last round of units
-  // leaves at most 1/16 of the warps idle, else the one that leaves fewest.
-  const int units = (p.w.nt + MT - 1) / MT, slots = 8 * kCtas * num_sms;
+// Warps per unit: the smallest power of two whose last round of units leaves
+// at most 1/16 of the warps idle, else the one that leaves fewest.
+int warps_per_unit(int units, int kc, int slots) {
   int S = 1;
   double best = 0.0;
-  for (int c = 1; c <= 8 && c <= p.w.kc; c *= 2) {
+  for (int c = 1; c <= 8 && c <= kc; c *= 2) {
     const int rounds = (units * c + slots - 1) / slots;
     const double used = (double)units * c / ((double)rounds * slots);
     if (used > best) S = c, best = used;
     if (best > 0.9375) break;
   }
-  const int per = 8 / S;
-  const int grid = min((units + per - 1) / per, kCtas * num_sms);
-  return launch_overlapped(small_kernel<NT, MT, ST, kCtas, kQ8>, dim3(grid), dim3(256), kRing + (S > 1 ? kPart : 0), s, p, S);
+  return S;
 }
+
+constexpr int kDotSmem = 64 * 1024;  // largest x area of dot_kernel
+
+template <int MT, int ST, int kCtas>
+struct Variant {
+  void (*kernel)(SmallParams, int);
+  int x_bytes;  // largest shared-memory area for x
+  int part;     // bytes of the partial sums when warps share a unit
+};
+
+// A kernel variant: one tile per unit and eight stages at two CTAs per SM for
+// the dot products (28.3 us at 2048 x 131073; two tiles: 29.9, six stages at
+// three CTAs: 30.1).  `call` is what to do with it.
+template <int TT, bool kQ8, typename F>
+cudaError_t with_dot(F&& call) {
+  constexpr int MT = 1, ST = 8, kCtas = 2;
+  return call(Variant<MT, ST, kCtas>{dot_kernel<TT, MT, ST, kCtas, kQ8>, kDotSmem, 8 * MT * TT * 64});
+}
+template <int NT, int MT, int ST, bool kQ8, typename F>
+cudaError_t with_small(F&& call) {
+  constexpr int kCtas = 2;
+  return call(Variant<MT, ST, kCtas>{small_kernel<NT, MT, ST, kCtas, kQ8>, 0, 8 * MT * NT * 512});
+}
+
+struct SetSmem {
+  template <int MT, int ST, int kCtas>
+  cudaError_t operator()(const Variant<MT, ST, kCtas>& v) const {
+    return cudaFuncSetAttribute(v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Stream<MT, ST>::kBytes + v.x_bytes + v.part);
+  }
+};
+// The shared-memory limits of every variant, on the current device.
+cudaError_t small_init() {
+  cudaError_t e = with_dot<1, false>(SetSmem());
+  if (e == cudaSuccess) e = with_dot<2, false>(SetSmem());
+  if (e == cudaSuccess) e = with_dot<1, true>(SetSmem());
+  if (e == cudaSuccess) e = with_dot<2, true>(SetSmem());
+  if (e == cudaSuccess) e = with_dot<4, true>(SetSmem());
+  if (e == cudaSuccess) e = with_small<1, 1, 8, false>(SetSmem());
+  if (e == cudaSuccess) e = with_small<1, 2, 4, false>(SetSmem());
+  if (e == cudaSuccess) e = with_small<2, 2, 4, false>(SetSmem());
+  if (e == cudaSuccess) e = with_small<1, 1, 8, true>(SetSmem());
+  if (e == cudaSuccess) e = with_small<1, 2, 4, true>(SetSmem());
+  if (e == cudaSuccess) e = with_small<2, 2, 4, true>(SetSmem());
+  return e;
+}
+
+struct Launch {
+  const SmallParams& p;
+  int x_bytes, num_sms;
+  cudaStream_t s;
+  template <int MT, int ST, int kCtas>
+  cudaError_t operator()(const Variant<MT, ST, kCtas>& v) const {
+    const int units = (p.w.nt + MT - 1) / MT;
+    const int S = warps_per_unit(units, p.w.kc, 8 * kCtas * num_sms), per = 8 / S;
+    const int grid = min((units + per - 1) / per, kCtas * num_sms);
+    return launch_overlapped(v.kernel, dim3(grid), dim3(256), Stream<MT, ST>::kBytes + x_bytes + (S > 1 ? v.part : 0),
+                             s, p, S);
+  }
+};
 
 template <bool kQ8>
 cudaError_t launch_small(const SmallParams& p, int num_sms, cudaStream_t s) {
+  const int tt = p.T <= 2 ? p.T : 4, x_bytes = tt * p.w.kc * (kTileK / 8) * (kQ8 ? 16 : 24);
+  if (p.T <= (kQ8 ? 4 : 2) && x_bytes <= kDotSmem) {
+    prof::Scope scope(kQ8 ? "linear_dot_q8" : "linear_dot", s);
+    const Launch go{p, x_bytes, num_sms, s};
+    if (tt == 1) return with_dot<1, kQ8>(go);
+    if (tt == 2) return with_dot<2, kQ8>(go);
+    if constexpr (kQ8) return with_dot<4, true>(go);
+  }
   prof::Scope scope(kQ8 ? "linear_small_q8" : "linear_small", s);
-  static const int v = getenv("LV") ? atoi(getenv("LV")) : 0;
-  if (p.T <= 8) {
-    if (v == 1) return launch_small_as<1, 1, 6, 3, kQ8>(p, num_sms, s);
-    if (v == 2) return launch_small_as<1, 2, 4, 2, kQ8>(p, num_sms, s);
-    if (v == 3) return launch_small_as<1, 1, 4, 4, kQ8>(p, num_sms, s);
-    if (v == 4) return launch_small_as<1, 2, 3, 3, kQ8>(p, num_sms, s);
-    return launch_small_as<1, 1, 8, 2, kQ8>(p, num_sms, s);
-  }
-  if (p.T <= 16) {
-    if (v == 1) return launch_small_as<2, 1, 6, 2, kQ8>(p, num_sms, s);
-    if (v == 2) return launch_small_as<2, 2, 5, 1, kQ8>(p, num_sms, s);
-    return launch_small_as<2, 2, 4, 2, kQ8>(p, num_sms, s);
-  }
-  if (v == 1) return launch_small_as<4, 4, 4, 1, kQ8>(p, num_sms, s);
-  if (v == 2) return launch_small_as<4, 2, 6, 1, kQ8>(p, num_sms, s);
-  return launch_small_as<4, 2, 4, 2, kQ8>(p, num_sms, s);
+  const Launch go{p, 0, num_sms, s};
+  if (p.T > 8) return with_small<2, 2, 4, kQ8>(go);
+  // two tiles per unit share the loads of x, where there are enough of them
+  // (1 token, 2048 inputs: 2.3 against 2.7 us at 2048 outputs, 37 against 33 at
+  // 131073)
+  return p.w.nt >= 2 * num_sms ? with_small<1, 2, 4, kQ8>(go) : with_small<1, 1, 8, kQ8>(go);
 }
 
 // ------------------------------------------------------------ entry points
@@ -417,6 +667,7 @@ moe_status create(const moe_linear_config* c, const moe_linear_weights* w, int o
   if (!L) return fail(MOE_ERR_OOM, "out of host memory");
   L->cfg = *c;
   cudaError_t e = cudaGetDevice(&L->device);
+  if (e == cudaSuccess) e = small_init();
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&L->num_sms, cudaDevAttrMultiProcessorCount, L->device);
   if (e != cudaSuccess) {
     delete L;
@@ -474,9 +725,17 @@ moe_status create(const moe_linear_config* c, const moe_linear_weights* w, int o
   return MOE_OK;
 }
 
+// 9 to 16 tokens: the mma.sync kernel starts about 4 us sooner than the GEMM
+// with its operand pass, but takes 0.21 us per million weights against 0.12
+// (measured at 16 tokens: 9.1 against 10.3 us at 4096 x 8192, 58 against 38 us
+// at 2048 x 131073).
+bool use_gemm(const moe_linear* L, int T) {
+  return T > kSmallTokens || (T > kExactTokens && (long long)L->w.N * L->w.K > 48000000ll);
+}
+
 moe_status run(moe_linear* L, const XIn& in, int T, void* y, void* stream) {
   cudaStream_t s = (cudaStream_t)stream;
-  if (T > kSmallTokens) return launch_gemm(L, in, T, static_cast<uint16_t*>(y), s);
+  if (use_gemm(L, T)) return launch_gemm(L, in, T, static_cast<uint16_t*>(y), s);
   SmallParams p = {};
   p.w = L->w;
   p.T = T;

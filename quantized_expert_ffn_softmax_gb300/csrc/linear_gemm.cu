@@ -1,4 +1,4 @@
-// moe_linear on batches above kSmallTokens: tcgen05 GEMM with the 4-bit
+// moe_linear on larger batches (linear.cu says which): tcgen05 GEMM with the 4-bit
 // weights dequantised on the way into shared memory.
 //
 //   prep   x (bf16, or 8-bit codes with scales) -> x16: fp16, every token
@@ -7,16 +7,24 @@
 //   gemm   D[128 rows of W x BN tokens] = W' x16^T in TMEM, fp32; epilogue
 //          y = D * row factor * token factor + bias, one rounding to bf16
 //
-// W' = (code - 8) * s' is rounded once to fp16 (relative 2^-12): a code in
-// bits 3-6 of a zero half word reads code * 2^-21 (an fp16 subnormal), so one
-// fp16 FMA with s = s' * 2^21, which is how the scales are stored, and -8 s'
-// gives the weight with a single rounding.
+// W' = (code - 8) * s' is rounded once to fp16 (2^-11 of itself at most): a
+// code in the low bits of a zero half word reads code * 2^-24 (an fp16
+// subnormal), in the next four code * 2^-20, so one fp16 FMA with s' * 2^24,
+// which is how the scales are stored, or s' * 2^20, and -8 s' gives the weight
+// with a single rounding and without a conversion.
 //
-// One CTA per SM, warp-specialised.  Warps 0-3: epilogue.  Warps 4-11:
-// producers, each streams the tiles of its own 16 rows through a ring of its
-// own (16-byte asynchronous copies) and writes fp16 rows into the stage's A
-// tile (128-byte swizzle, K-major).  Warp 12: TMA of the x16 tile.  Warp 13:
-// MMA issue.  Few row blocks: S CTAs of a cluster share one output tile, each
+// Operand A (the weights) goes through tensor memory for tiles of up to 128
+// tokens (kTs) and through shared memory above: read from shared memory an MMA
+// takes about 110 cycles however few its tokens (897 cycles for the 8 of a
+// stage at 16 to 64 tokens), from tensor memory its time falls with N; but
+// tensor memory holds A stages beside two accumulators only up to 128 tokens.
+//
+// One CTA per SM, warp-specialised, 128 inputs per stage.  Warps 0-7:
+// epilogue (two per TMEM lane quarter, taking turns by 16 tokens).  Then 8 or
+// 16 producers: each turns its 16 rows of a packed tile into fp16 rows of the
+// stage's A tile; 16 take turns by stage.  Then
+// one warp each for the TMA of the packed tiles (8 row tiles in one copy, into
+// a ring), the TMA of the x16 tile and the MMAs.  Few row blocks: S CTAs of a cluster share one output tile, each
 // with a part of K, and sum their fp32 tiles through distributed shared
 // memory in rank order.
 #include <string.h>
@@ -36,21 +44,24 @@ using namespace dev;
 using namespace op;
 
 constexpr int kRowsA = 128;               // rows of W per tile
-constexpr int kStepK = 64;                // inputs per stage
-constexpr int kABytes = kRowsA * 128;     // A tile of a stage
-constexpr int kProdWarps = 8;
-constexpr int kLoadWarp = 4 + kProdWarps;
-constexpr int kMmaWarp = kLoadWarp + 1;
-constexpr int kThreads = (kMmaWarp + 1) * 32;
-constexpr int kRing = 6;                  // packed tiles in flight per producer warp
-constexpr int kRingBytes = kProdWarps * kRing * kTileBytes;
-constexpr int kMaxStages = 8;
-constexpr int kBarBytes = 256;
+constexpr int kHalfA = kRowsA * 128;      // bytes of 64 inputs of the A tile
+constexpr int kABytes = 2 * kHalfA;       // A tile of a stage (128 inputs)
+constexpr int kRowTiles = kRowsA / kTileRows;  // 8: producers per stage
+constexpr int kMaxStages = 6;
+constexpr int kTsTokens = 128;                 // largest tile with A in tensor memory
+constexpr int kBarBytes = 512;
+constexpr int kXfBytes = 256 * 4;
 constexpr int kMaxSmem = 227 * 1024;
+constexpr int kEpiWarps = 8;
+constexpr int kRaw = kRowTiles * kTileBytes;   // packed weights of a stage
+constexpr int kMaxRing = 16;
+constexpr int threads(int prod) { return (kEpiWarps + prod + 3) * 32; }
 
 // ------------------------------------------------------------ prep
+// perm: inside every block of 32 inputs, pair i of the 8 inputs 8 t .. 8 t + 7
+// goes to pair 4 i + t, the order in which A fragments lie in tensor memory.
 template <bool kQ8, int V>
-__global__ void __launch_bounds__(1024) prep_kernel(const XIn in, int K, __half* __restrict__ x16,
+__global__ void __launch_bounds__(1024) prep_kernel(const XIn in, int K, bool perm, __half* __restrict__ x16,
                                                     float* __restrict__ x_f) {
   __shared__ uint32_t red[32];
   dep_wait();
@@ -96,7 +107,13 @@ __global__ void __launch_bounds__(1024) prep_kernel(const XIn in, int K, __half*
       __half2 h[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) h[k] = __floats2half2_rn(v[j][2 * k] * f, v[j][2 * k + 1] * f);
-      *reinterpret_cast<uint4*>(x16 + (size_t)t * K + 8 * i) = *reinterpret_cast<const uint4*>(h);
+      if (perm) {
+        __half2* o = reinterpret_cast<__half2*>(x16 + (size_t)t * K + 32 * (i >> 2)) + (i & 3);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[4 * k] = h[k];
+      } else {
+        *reinterpret_cast<uint4*>(x16 + (size_t)t * K + 8 * i) = *reinterpret_cast<const uint4*>(h);
+      }
     }
   }
   if (threadIdx.x == 0) x_f[t] = pow2f(e);
@@ -113,49 +130,107 @@ struct GemmParams {
   int units;     // row blocks x token tiles
   int split;     // CTAs of a cluster that share a unit (1: units are walked persistently)
   int stages;
+  int ring;
   int tmem_cols;
   int* err;
   unsigned long long timeout_ns;
 };
 
-// Word of 8 codes -> 8 weights (code - 8) s' as fp16, in input order.
-// s: the stored scale s' 2^21 in both halves, c: -8 s'.
-__device__ __forceinline__ uint4 dequant8(uint32_t w, __half2 s, __half2 c) {
-  uint32_t v[4] = {w & 0x00780078u, (w >> 4) & 0x00780078u, (w >> 8) & 0x00780078u,
-                   __funnelshift_r(w, w, 12) & 0x00780078u};
+// Word of 8 codes -> 8 weights (code - 8) s' as fp16, in input order; s24, s20
+// and c: s' 2^24 (the stored scale), s' 2^20 and -8 s' in both halves.
+__device__ __forceinline__ uint4 dequant8(uint32_t w, __half2 s24, __half2 s20, __half2 c) {
+  const uint32_t w8 = w >> 8;
+  const uint32_t v[4] = {w & 0x000F000Fu, w & 0x00F000F0u, w8 & 0x000F000Fu, w8 & 0x00F000F0u};
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&v[i]), s, c);
+    const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&v[i]), (i & 1) ? s20 : s24, c);
     o[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+// Two words of one row, blocks b and b + 1, whose scales are the halves of q.
+__device__ __forceinline__ void dequant16(uint32_t wa, uint32_t wb, uint32_t q, uint4& da, uint4& db) {
+  const __half2 s24 = *reinterpret_cast<const __half2*>(&q);
+  const __half2 s20 = __hmul2(s24, __half2half2(__ushort_as_half(0x2C00)));  // * 2^-4
+  const __half2 c = __hmul2(s24, __half2half2(__ushort_as_half(0x8008)));    // * -2^-21
+  da = dequant8(wa, __low2half2(s24), __low2half2(s20), __low2half2(c));
+  db = dequant8(wb, __high2half2(s24), __high2half2(s20), __high2half2(c));
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t saddr, int rank) {
-  float v;
+
+// Cluster barriers.  A release by every warp costs about 570 cycles each, one
+// after the other (27 warps: 8 us); so the CTA meets first and one warp
+// releases for all (its release covers what it observed through the CTA
+// barrier).
+__device__ __forceinline__ void cluster_publish(int warp) {
+  __syncthreads();
+  if (warp == 0)
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  else
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Only orders exits after reads whose values have already been used.
+__device__ __forceinline__ void cluster_leave() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// 16 bytes of the shared memory of cluster rank `rank` at this CTA's address.
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t saddr, int rank) {
+  float4 v;
   asm volatile(
-      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}\n"
-      : "=f"(v)
-      : "r"(saddr), "r"(rank)
-      : "memory");
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %4, %5;\n ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [a];\n}\n"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(saddr), "r"(rank));
   return v;
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
-    gemm_kernel(const __grid_constant__ GemmParams p, const __grid_constant__ CUtensorMap xmap) {
+// On an error path a stage may stay incomplete: gives the copies already
+// issued time to land before the CTA can exit.
+__device__ __forceinline__ void settle(int* err) {
+  if (__any_sync(0xffffffffu, ld_relaxed_i32(err) != 0)) {
+    const uint64_t t0 = global_timer();
+    while (global_timer() - t0 < 200000ull) {
+    }
+  }
+  __syncwarp();
+}
+
+// This warp's 16 lanes from taddr, 64 columns: thread 4 g + t writes column
+// 4 j + t of lane g from r[2 j] and of lane g + 8 from r[2 j + 1].
+__device__ __forceinline__ void tmem_st_16x128b_x16(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// kProd: producer warps (8 or 16).  kTs: operand A in tensor memory.
+template <int kProd, bool kTs>
+__global__ void __launch_bounds__(threads(kProd), 1)
+    gemm_kernel(const __grid_constant__ GemmParams p, const __grid_constant__ CUtensorMap xmap,
+                const __grid_constant__ CUtensorMap wmap) {
+  constexpr int kProd0 = kEpiWarps, kRawWarp = kProd0 + kProd, kLoadWarp = kRawWarp + 1, kMmaWarp = kLoadWarp + 1;
+  constexpr int kTurns = kProd / kRowTiles;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                          ~static_cast<uintptr_t>(1023));
   const int bn = p.bn, S = p.stages;
-  const int stage_bytes = kABytes + bn * 128;
-  unsigned char* ring0 = smem + S * stage_bytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring0 + kRingBytes);
+  constexpr int kA = kTs ? 0 : kABytes;  // bytes of A in a stage
+  const int half_b = bn * 128, stage_bytes = kA + 2 * half_b;
+  const int R = p.ring;
+  unsigned char* raw = smem + S * stage_bytes;  // R packed tiles of 128 rows x 128 inputs
+  float* xf = reinterpret_cast<float*>(raw + R * kRaw);  // [256] token factors
+  uint64_t* full = reinterpret_cast<uint64_t*>(xf + 256);
   uint64_t* empty = full + kMaxStages;
-  uint64_t* tfull = empty + kMaxStages;
+  uint64_t* raw_full = empty + kMaxStages;
+  uint64_t* raw_empty = raw_full + kMaxRing;
+  uint64_t* tfull = raw_empty + kMaxRing;
   uint64_t* tempty = tfull + 2;
   uint64_t* tdrain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tdrain + 1);
@@ -163,12 +238,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], kProdWarps + 1);  // + the loader's arrive with the tile's bytes
+      mbar_init(&full[s], kRowTiles + 1);  // + the loader's arrive with the tile's bytes
       mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < R; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], kRowTiles);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 4 * 32);
+      mbar_init(&tempty[b], kEpiWarps * 32);
     }
     mbar_init(tdrain, 1);
     fence_mbar_init();
@@ -183,193 +262,242 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const uint64_t tmo = p.timeout_ns;
 
-  // this CTA's units, and its part of K in packed tiles (128 inputs) and steps
+  // this CTA's units, and its part of K in packed tiles (128 inputs, a stage)
   const int split = p.split, rank = split > 1 ? (int)(blockIdx.x % split) : 0;
   const int u0 = blockIdx.x / split, ustep = split > 1 ? p.units : gridDim.x;
   const int kc = p.w.kc;
   const int c0 = rank * kc / split, c1 = (rank + 1) * kc / split;
-  const int steps = min(2 * c1, (p.w.K + kStepK - 1) / kStepK) - 2 * c0;
+  const int total = (p.units - u0 + ustep - 1) / ustep * (c1 - c0);  // stages of this CTA
 
-  if (warp < 4) {
+  if (warp < kEpiWarps) {
     // ------------------------------------------------------------ epilogue
-    // Thread r owns row r of the tile (TMEM lane r).
+    // Thread r owns row r of the tile (TMEM lane r); the two warps of a lane
+    // quarter take alternate groups of 16 tokens.
     dep_wait();
     dep_release();
-    const int r = warp * 32 + lane;
+    // With A in tensor memory lane 16 w + g holds the row of fragment row g.
+    const int r = (warp & 3) * 32 + lane, c_first = 16 * (warp >> 2);
+    const int rr = kTs ? (r & ~7) + frag_row(r & 7) : r;
+    const size_t N = p.w.N;
     int j = 0;
     for (int u = u0; u < p.units; u += ustep, ++j) {
-      const int row = (u % p.n_rb) * kRowsA + r, t0 = (u / p.n_rb) * bn;
+      const int row = (u % p.n_rb) * kRowsA + rr, t0 = (u / p.n_rb) * bn;
       const int nt = min(bn, p.T - t0);
       const int b = j & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(&tfull[b], (j >> 1) & 1, p.err, tmo))) break;
+      // token factors of the tile (the warps agree on going on: the named
+      // barrier waits for all of them)
+      named_bar_sync(1, kEpiWarps * 32);
+      if (threadIdx.x < bn) xf[threadIdx.x] = (int)threadIdx.x < nt ? p.x_f[t0 + threadIdx.x] : 0.0f;
+      const bool ok = __all_sync(0xffffffffu, mbar_wait(&tfull[b], (j >> 1) & 1, p.err, tmo));
+      if (!named_bar_and(1, kEpiWarps * 32, ok)) break;
       tc_fence_after();
-      const uint32_t tb = tmem + ((uint32_t)(warp * 32) << 16) + (uint32_t)(b * bn);
+      const uint32_t tb = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(b * bn);
       if (split == 1) {
         const bool in = row < p.w.N;
-        const float rf = in ? __ldg(p.w.row_f + row) * 0x1p21f : 0.0f;
+        const float rf = in ? __ldg(p.w.row_f + row) * 0x1p24f : 0.0f;
         const float bias = in && p.w.bias ? __ldg(p.w.bias + row) : 0.0f;
-        for (int c = 0; c < nt; c += 16) {
+        for (int c = c_first; c < nt; c += 16 * (kEpiWarps / 4)) {
           uint32_t v[16];
           tmem_ld16(tb + c, v);
-          tmem_wait_ld();
+          float f[16];  // (read before the stores: a load between them would wait for them)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int t = t0 + c + i;
-            if (in && c + i < nt)
-              p.y[(size_t)t * p.w.N + row] = __bfloat16_as_ushort(
-                  __float2bfloat16_rn(fmaf(__uint_as_float(v[i]) * rf, p.x_f[t], bias)));
+          for (int i = 0; i < 16; i += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(xf + c + i);
+            f[i] = q.x, f[i + 1] = q.y, f[i + 2] = q.z, f[i + 3] = q.w;
+          }
+          uint16_t* yr = p.y + (size_t)(t0 + c) * N + row;
+          tmem_wait_ld();
+          uint32_t o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            o[i] = pack_bf16(fmaf(__uint_as_float(v[2 * i]) * rf, f[2 * i], bias),
+                             fmaf(__uint_as_float(v[2 * i + 1]) * rf, f[2 * i + 1], bias));
+          if (in && c + 16 <= nt) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i, yr += N) *yr = (uint16_t)(i & 1 ? o[i / 2] >> 16 : o[i / 2]);
+          } else if (in) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i, yr += N)
+              if (c + i < nt) *yr = (uint16_t)(i & 1 ? o[i / 2] >> 16 : o[i / 2]);
           }
         }
       } else {
         // the tile as [token][128 rows] fp32 over the stages (all MMAs are done)
         float* part = reinterpret_cast<float*>(smem);
-        for (int c = 0; c < nt; c += 16) {
+        for (int c = c_first; c < nt; c += 16 * (kEpiWarps / 4)) {
           uint32_t v[16];
           tmem_ld16(tb + c, v);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) part[(c + i) * kRowsA + r] = __uint_as_float(v[i]);
+          for (int i = 0; i < 16; ++i) part[(c + i) * kRowsA + rr] = __uint_as_float(v[i]);
         }
       }
       tc_fence_before();
       mbar_arrive(&tempty[b]);
     }
-  } else if (warp < kLoadWarp) {
+  } else if (warp < kRawWarp) {
     // ------------------------------------------------------------ producers
-    const int w = warp - 4, g = lane >> 2, t = lane & 3;
-    unsigned char* ring = ring0 + w * kRing * kTileBytes;
-    int lu = u0, lc = c0;
-    const uint8_t* lsrc = nullptr;
-    auto source = [&]() {
-      const int tile = min((lu % p.n_rb) * (kRowsA / kTileRows) + w, p.w.nt - 1);  // past N: not stored
-      lsrc = p.w.tiles + ((size_t)tile * kc + c0) * kTileBytes + 16 * lane;
-    };
-    source();
-    uint32_t ldst = smem_u32(ring) + 16 * lane;
-    const uint32_t lend = ldst + kRing * kTileBytes;
-    auto issue = [&]() {
-      if (lu < p.units) {
-        cp_async_16(ldst, lsrc);
-        cp_async_16(ldst + 512, lsrc + 512);
-        if (lane < 8) cp_async_16(ldst + kTileCodes, lsrc + kTileCodes);
-        lsrc += kTileBytes;
-        if (++lc == c1) {
-          lc = c0;
-          lu += ustep;
-          source();
-        }
-      }
-      cp_async_commit();
-      ldst += kTileBytes;
-      if (ldst == lend) ldst -= kRing * kTileBytes;
-    };
-#pragma unroll
-    for (int i = 0; i < kRing - 1; ++i) issue();  // the weights are the library's own: nothing to wait for
     dep_wait();
     dep_release();
-    int slot = 0, st = 0;
-    uint32_t par = 1;  // parity of the stage's next "empty" phase
-    bool alive = true;
-    // rows g and g + 8 of the warp's 16: 16-byte chunk 4 b + t of the row for
-    // block b, XOR-swizzled by the row; odd rows store their blocks in the
-    // other order, so that eight lanes touch eight different chunks
-    const uint32_t a_row = (uint32_t)((16 * w + g) * 128);
-    const uint32_t o0 = a_row + (uint32_t)(((4 * (g & 1) + t) ^ g) * 16);
-    const uint32_t o1 = a_row + (uint32_t)(((4 * ((g & 1) ^ 1) + t) ^ g) * 16);
-    for (int u = u0; u < p.units && alive; u += ustep) {
-      for (int s2 = 0; s2 < steps && alive; s2 += 2) {
-        cp_async_wait<kRing - 2>();
-        __syncwarp();  // the tile is there for every lane, and every lane is done with the one before
-        issue();
-        const unsigned char* tl = ring + slot * kTileBytes;
-        slot = slot + 1 == kRing ? 0 : slot + 1;
-        const uint4 sc = *reinterpret_cast<const uint4*>(tl + kTileCodes + 16 * g);
-        const __half2 k8 = __half2half2(__ushort_as_half(0x8040));  // -2^-18
+    // The row tile: any, or with A in tensor memory one of the two whose lanes
+    // the warp can reach.
+    const int pw = warp - kProd0, g = lane >> 2, t = lane & 3;
+    const int w = kTs ? 2 * (warp & 3) + ((pw >> 2) & 1) : pw & (kRowTiles - 1), turn = pw / kRowTiles;
+    // ring slot and stage of every kTurns-th packed tile, with the parities of
+    // the phases to wait for
+    int slot = turn, st = turn;
+    uint32_t rpar = 0, par = 1;
+    // rows frag_row(g) and + 8 of the warp's 16, 16-byte chunk 4 b + t of 64
+    // inputs for block b, XOR-swizzled by the row
+    const int fr = frag_row(g);
+    const uint32_t o0 = (uint32_t)((16 * w + fr) * 128 + (t ^ fr) * 16), o1 = o0 ^ 64;
+    const unsigned char* mine = raw + w * kTileBytes;
+    for (int i = turn; i < total; i += kTurns) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&raw_full[slot], rpar, p.err, tmo))) break;
+      const unsigned char* tl = mine + slot * kRaw;
+      const uint4 w0 = *reinterpret_cast<const uint4*>(tl + 16 * lane);
+      const uint4 w1 = *reinterpret_cast<const uint4*>(tl + 512 + 16 * lane);
+      const uint4 sc = *reinterpret_cast<const uint4*>(tl + kTileCodes + 16 * g);
+      // row frag_row(g) (even) and + 8 (odd) of block 0 .. 3: pair i of block b
+      // at o[8 b + 2 i] and o[8 b + 2 i + 1], its column 16 b + 4 i + t
+      uint32_t o[32];
+      auto put = [&](int b, uint32_t wa, uint32_t wb, uint32_t q, int row) {
+        uint4 da, db;
+        dequant16(wa, wb, q, da, db);
+        uint32_t* d = o + 8 * b + row;
+        d[0] = da.x, d[2] = da.y, d[4] = da.z, d[6] = da.w;
+        d[8] = db.x, d[10] = db.y, d[12] = db.z, d[14] = db.w;
+      };
+      put(0, w0.x, w0.z, sc.x, 0);
+      put(0, w0.y, w0.w, sc.z, 1);
+      put(2, w1.x, w1.z, sc.y, 0);
+      put(2, w1.y, w1.w, sc.w, 1);
+      // the ring slot's reads come before the next copy into it
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&raw_empty[slot]);
+      slot += kTurns;
+      if (slot >= R) slot -= R, rpar ^= 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], par, p.err, tmo))) break;
+      if constexpr (kTs) {
+        tc_fence_after();
+        tmem_st_16x128b_x16(tmem + ((uint32_t)(16 * w) << 16) + (uint32_t)(2 * bn + 64 * st), o);
+        tmem_wait_st();
+        tc_fence_before();
+      } else {
+        unsigned char* A = smem + st * stage_bytes;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (s2 + h >= steps) break;
-          const uint4 wd = *reinterpret_cast<const uint4*>(tl + 512 * h + 16 * lane);
-          const uint32_t s0 = h ? sc.y : sc.x, s1 = h ? sc.w : sc.z;
-          const __half2 q0 = *reinterpret_cast<const __half2*>(&s0), q1 = *reinterpret_cast<const __half2*>(&s1);
-          const __half2 a0 = __low2half2(q0), a1 = __high2half2(q0), b0 = __low2half2(q1), b1 = __high2half2(q1);
-          const uint4 r00 = dequant8(wd.x, a0, __hmul2(a0, k8)), r80 = dequant8(wd.y, b0, __hmul2(b0, k8));
-          const uint4 r01 = dequant8(wd.z, a1, __hmul2(a1, k8)), r81 = dequant8(wd.w, b1, __hmul2(b1, k8));
-          if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], par, p.err, tmo))) {
-            alive = false;
-            break;
-          }
-          unsigned char* A = smem + st * stage_bytes;
-          const bool odd = g & 1;
-          *reinterpret_cast<uint4*>(A + o0) = odd ? r01 : r00;
-          *reinterpret_cast<uint4*>(A + o0 + 1024) = odd ? r81 : r80;
-          *reinterpret_cast<uint4*>(A + o1) = odd ? r00 : r01;
-          *reinterpret_cast<uint4*>(A + o1 + 1024) = odd ? r80 : r81;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[st]);
-          if (++st == S) st = 0, par ^= 1;
+        for (int b = 0; b < 4; ++b) {
+          unsigned char* d = A + (b >> 1) * kHalfA + ((b & 1) ? o1 : o0);
+          *reinterpret_cast<uint4*>(d) = make_uint4(o[8 * b], o[8 * b + 2], o[8 * b + 4], o[8 * b + 6]);
+          *reinterpret_cast<uint4*>(d + 1024) = make_uint4(o[8 * b + 1], o[8 * b + 3], o[8 * b + 5], o[8 * b + 7]);
         }
+        fence_proxy_async_smem();  // the writes before the MMA's reads
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[st]);
+      st += kTurns;
+      if (st >= S) st -= S, par ^= 1;
+    }
+  } else if (warp == kRawWarp) {
+    // ------------------------------------------------------------ packed tiles
+    // The weights are the library's own: the first copies wait for nothing.
+    int slot = 0, i = 0;
+    uint32_t par = 1;
+    for (int u = u0; u < p.units && i >= 0; u += ustep) {
+      for (int c = c0; c < c1; ++c, ++i) {
+        if (i == R) {
+          dep_wait();
+          dep_release();
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(&raw_empty[slot], par, p.err, tmo))) {
+          i = -1 << 30;
+          break;
+        }
+        if (elect_one()) {
+          mbar_expect_tx(&raw_full[slot], kRaw);
+          tma_load_2d(raw + slot * kRaw, &wmap, c * (kTileBytes / 8), (u % p.n_rb) * kRowTiles, &raw_full[slot]);
+        }
+        __syncwarp();
+        if (++slot == R) slot = 0, par ^= 1;
       }
     }
-    cp_async_wait<0>();
+    if (i >= 0 && i <= R) {
+      dep_wait();
+      dep_release();
+    }
+    settle(p.err);
   } else if (warp == kLoadWarp) {
     // ------------------------------------------------------------ x16 tiles
     dep_wait();
     dep_release();
     int st = 0;
-    uint32_t par = 1, n = 0;
+    uint32_t par = 1;
     bool alive = true;
     for (int u = u0; u < p.units && alive; u += ustep) {
       const int t0 = (u / p.n_rb) * bn;
-      for (int s = 0; s < steps; ++s, ++n) {
+      for (int c = c0; c < c1; ++c) {
         if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], par, p.err, tmo))) {
           alive = false;
           break;
         }
         if (elect_one()) {
-          mbar_expect_tx(&full[st], (uint32_t)(bn * 128));
-          tma_load_2d(smem + st * stage_bytes + kABytes, &xmap, (2 * c0 + s) * kStepK, t0, &full[st]);
+          unsigned char* B = smem + st * stage_bytes + kA;
+          mbar_expect_tx(&full[st], (uint32_t)(2 * half_b));
+          tma_load_2d(B, &xmap, c * kTileK, t0, &full[st]);
+          tma_load_2d(B + half_b, &xmap, c * kTileK + 64, t0, &full[st]);  // past K: zeros
         }
         __syncwarp();
         if (++st == S) st = 0, par ^= 1;
       }
     }
-    // On an error path the producers may stop short of completing a phase:
-    // give the copies already issued time to land before the CTA exits.
-    if (__any_sync(0xffffffffu, ld_relaxed_i32(p.err) != 0)) {
-      const uint64_t w0 = global_timer();
-      while (global_timer() - w0 < 200000ull) {
-      }
-    }
-    __syncwarp();
+    settle(p.err);
   } else {
     // ------------------------------------------------------------ MMA issue
     dep_wait();
     dep_release();
+    // Everything a stage needs is kept incrementally: the instructions between
+    // two stages' MMAs are what leaves the tensor core idle on small tiles.
+    const uint32_t idesc = idesc_f16_m128(bn);
+    const uint64_t d0 = smem_desc_sw128(smem_u32(smem));
+    const uint64_t a1 = kHalfA >> 4, b0 = kA >> 4, b1 = b0 + (half_b >> 4), dstep = stage_bytes >> 4;
+    uint64_t da = d0;
     int st = 0, j = 0;
     uint32_t par = 0;
-    const uint32_t idesc = idesc_f16_m128(bn);
     for (int u = u0; u < p.units; u += ustep, ++j) {
       const int b = j & 1;
       if (!__all_sync(0xffffffffu, mbar_wait(&tempty[b], ((j >> 1) & 1) ^ 1, p.err, tmo))) break;
       tc_fence_after();
       const uint32_t d = tmem + (uint32_t)(b * bn);
       bool ok = true;
-      for (int s = 0; s < steps; ++s) {
+      uint32_t acc = 0;
+      for (int c = c0; c < c1; ++c) {
         if (!__all_sync(0xffffffffu, mbar_wait(&full[st], par, p.err, tmo))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t a = smem_u32(smem + st * stage_bytes);
-        const uint64_t da = smem_desc_sw128(a), db = smem_desc_sw128(a + kABytes);
         if (elect_one()) {
+          if constexpr (kTs) {
+            const uint32_t a = tmem + (uint32_t)(2 * bn + 64 * st);  // 16 inputs: 8 columns
+            umma_f16_ts(d, a, da, idesc, acc);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) umma_f16(d, da + 2 * k, db + 2 * k, idesc, (s | k) ? 1u : 0u);
+            for (int k = 1; k < 4; ++k) umma_f16_ts(d, a + 8 * k, da + 2 * k, idesc, 1u);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) umma_f16_ts(d, a + 32 + 8 * k, da + b1 + 2 * k, idesc, 1u);
+          } else {
+            umma_f16(d, da, da + b0, idesc, acc);
+#pragma unroll
+            for (int k = 1; k < 4; ++k) umma_f16(d, da + 2 * k, da + b0 + 2 * k, idesc, 1u);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) umma_f16(d, da + a1 + 2 * k, da + b1 + 2 * k, idesc, 1u);
+          }
           umma_commit(&empty[st]);
         }
         __syncwarp();
-        if (++st == S) st = 0, par ^= 1;
+        acc = 1;
+        da += dstep;
+        if (++st == S) st = 0, par ^= 1, da = d0;
       }
       if (!ok) break;
       if (elect_one()) umma_commit(&tfull[b]);
@@ -386,27 +514,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (split > 1) {
-    __syncwarp();
-    cluster_sync();  // every partial tile is in its CTA's shared memory
-    if (warp < 4) {
-      const int r = warp * 32 + lane;
-      const int row = (u0 % p.n_rb) * kRowsA + r, t0 = (u0 / p.n_rb) * bn;
-      const int nt = min(bn, p.T - t0);
-      if (row < p.w.N) {
-        const float rf = __ldg(p.w.row_f + row) * 0x1p21f;
-        const float bias = p.w.bias ? __ldg(p.w.bias + row) : 0.0f;
-        const uint32_t part = smem_u32(smem) + 4 * r;
-        for (int c = rank; c < nt; c += split) {
-          float v = 0.0f;
-          for (int k = 0; k < split; ++k) v += ld_cluster_f32(part + c * kRowsA * 4, k);
-          const int t = t0 + c;
-          p.y[(size_t)t * p.w.N + row] =
-              __bfloat16_as_ushort(__float2bfloat16_rn(fmaf(v * rf, p.x_f[t], bias)));
-        }
-      }
+    cluster_publish(warp);  // every partial tile is in its CTA's shared memory
+    // this CTA sums the tokens congruent to its rank, four rows per thread
+    const int t0 = (u0 / p.n_rb) * bn, nt = min(bn, p.T - t0);
+    const int row = (u0 % p.n_rb) * kRowsA + 4 * lane;
+    float rf[4], bias[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool in = row + i < p.w.N;
+      rf[i] = in ? __ldg(p.w.row_f + row + i) * 0x1p24f : 0.0f;
+      bias[i] = in && p.w.bias ? __ldg(p.w.bias + row + i) : 0.0f;
     }
-    __syncwarp();
-    cluster_sync();  // no CTA leaves while its tile is read
+    const uint32_t part = smem_u32(smem) + 16 * lane;
+    for (int c = rank + split * warp; c < nt; c += split * (kMmaWarp + 1)) {
+      const float f = p.x_f[t0 + c];
+      float4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = k < split ? ld_cluster_f4(part + c * kRowsA * 4, k) : make_float4(0, 0, 0, 0);
+      float a[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int k = 1; k < 8; ++k) a[0] += v[k].x, a[1] += v[k].y, a[2] += v[k].z, a[3] += v[k].w;
+      uint16_t* yr = p.y + (size_t)(t0 + c) * p.w.N + row;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (row + i < p.w.N) yr[i] = __bfloat16_as_ushort(__float2bfloat16_rn(fmaf(a[i] * rf[i], f, bias[i])));
+    }
+    cluster_leave();  // no CTA leaves while its tile is read
   }
   tc_fence_before();
   __syncthreads();
@@ -418,14 +551,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Shape of a launch.
 struct Plan {
-  int bn, units, split, stages, smem, tmem_cols;
+  bool ts;
+  int bn, units, split, prod, stages, ring, smem, tmem_cols;
 };
 
+// slots[i]: clusters of 2^i CTAs that run at once (an SM holds one CTA; GPCs
+// whose SM count is no multiple leave some out: 16 clusters of 8 do not fit).
 // Tokens per tile and CTAs per tile, by an estimate of the time in cycles:
-// a step of 64 inputs takes 2 cycles per token on the tensor core and about
-// 170 in the producers, whichever is longer; 2500 cycles per tile for its
-// start and epilogue, 1500 more for the sum over a cluster.
-Plan plan(int N, int kc, int T, int num_sms) {
+// a step of 64 inputs takes 2 cycles per token on the tensor core (440 at
+// least with A in shared memory) and about 200 in the producers, whichever is
+// longer; 2500 cycles per tile for its start and epilogue, 1500 more for the
+// sum over a cluster.
+Plan plan(int N, int kc, int T, const int (&slots)[4]) {
   Plan best = {};
   double best_t = 0.0;
   const int rb = (N + kRowsA - 1) / kRowsA;
@@ -436,11 +573,12 @@ Plan plan(int N, int kc, int T, int num_sms) {
     const int tt = (T + bn - 1) / bn;
     if ((long long)rb * tt > 0x3fffffff) break;
     const int units = rb * tt;
-    for (int split = 1; split <= 8 && split <= kc; split *= 2) {
-      if (split > 1 && units * split > num_sms) break;
-      const int rounds = (units * split + num_sms - 1) / num_sms;
+    for (int i = 0; i < 4 && (1 << i) <= kc; ++i) {
+      const int split = 1 << i;
+      if (i && units > slots[i]) break;
+      const int rounds = (units + slots[i] - 1) / slots[i];
       const double steps = 2.0 * ((kc + split - 1) / split);
-      const double t = rounds * (steps * std::max(2 * bn, 170) + 2500) + (split > 1 ? 1500 : 0);
+      const double t = rounds * (steps * std::max(2 * bn, bn > kTsTokens ? 440 : 200) + 2500) + (split > 1 ? 1500 : 0);
       if (best_t == 0.0 || t < best_t) {
         best_t = t;
         best.bn = bn;
@@ -449,40 +587,54 @@ Plan plan(int N, int kc, int T, int num_sms) {
       }
     }
   }
-  const int stage = kABytes + best.bn * 128;
-  best.stages = std::min(kMaxStages, (kMaxSmem - 1024 - kRingBytes - kBarBytes) / stage);
-  best.smem = best.stages * stage + kRingBytes + kBarBytes + 1024;
-  // (S stages always hold the fp32 tile of a shared unit: S >= 3 up to 256
-  // tokens, and smaller tiles have at least that ratio)
-  best.tmem_cols = 32;
-  while (best.tmem_cols < 2 * best.bn) best.tmem_cols *= 2;
+  const int room = kMaxSmem - 1024 - kBarBytes - kXfBytes;
+  best.ts = best.bn <= kTsTokens;
+  best.tmem_cols = 512;
+  if (best.ts) {
+    const int stage = best.bn * 256;
+    best.prod = 16;
+    best.stages = std::min(kMaxStages, (512 - 2 * best.bn) / 64);
+    best.ring = std::min(kMaxRing, (room - best.stages * stage) / kRaw);
+    best.smem = best.stages * stage;
+  } else {
+    const int stage = kABytes + best.bn * 256;
+    // 16 producers where three stages fit beside a deep ring; else 8, whose
+    // rate is enough there (a stage then has 190 or more tokens of MMA work)
+    best.prod = room - 6 * kRaw >= 3 * stage ? 16 : 8;
+    best.ring = best.prod == 16 ? 6 : 3;
+    best.stages = std::min(kMaxStages, (room - best.ring * kRaw) / stage);
+    best.smem = best.stages * stage;
+  }
+  best.smem += best.ring * kRaw + kBarBytes + kXfBytes + 1024;
   return best;
 }
-static_assert(3 * (kABytes + 256 * 128) + kRingBytes + kBarBytes + 1024 <= kMaxSmem, "three stages at 256 tokens");
-static_assert(3 * (kABytes + 256 * 128) >= 256 * kRowsA * 4, "an fp32 tile fits in the stages");
-static_assert(8 * (2 * kMaxStages + 5) + 4 <= kBarBytes, "barriers");
+static_assert(2 * (kABytes + 256 * 256) + 3 * kRaw + kBarBytes + kXfBytes + 1024 <= kMaxSmem,
+              "two stages at 256 tokens");
+// two stages hold the fp32 tile of a shared unit: 2 (kABytes + 256 bn) >= 512 bn
+static_assert(8 * (2 * kMaxStages + 2 * kMaxRing + 5) + 4 <= kBarBytes, "barriers");
 
 template <bool kQ8>
-cudaError_t launch_prep(moe_linear* L, const XIn& in, int T, cudaStream_t s) {
+cudaError_t launch_prep(moe_linear* L, const XIn& in, int T, bool perm, cudaStream_t s) {
   prof::Scope scope(kQ8 ? "linear_prep_q8" : "linear_prep", s);
   const int nvec = L->w.K / 8;
   __half* x16 = static_cast<__half*>(L->x16);
   if (nvec <= 1024)
-    return launch_overlapped(prep_kernel<kQ8, 1>, dim3(T), dim3((nvec + 31) / 32 * 32), 0, s, in, L->w.K, x16, L->x_f);
-  return launch_overlapped(prep_kernel<kQ8, 4>, dim3(T), dim3(((nvec + 3) / 4 + 31) / 32 * 32), 0, s, in, L->w.K, x16,
+    return launch_overlapped(prep_kernel<kQ8, 1>, dim3(T), dim3((nvec + 31) / 32 * 32), 0, s, in, L->w.K, perm, x16,
+                             L->x_f);
+  return launch_overlapped(prep_kernel<kQ8, 4>, dim3(T), dim3(((nvec + 3) / 4 + 31) / 32 * 32), 0, s, in, L->w.K, perm, x16,
                            L->x_f);
 }
 
 }  // namespace
 
 size_t gemm_workspace(int K, int max_tokens) {
-  if (max_tokens <= kSmallTokens) return 0;
+  if (max_tokens <= kExactTokens) return 0;
   return (((size_t)max_tokens * K * 2 + 255) & ~(size_t)255) + (size_t)max_tokens * 4;
 }
 
 moe_status gemm_init(moe_linear* L, void* ws) {
   const int T = L->cfg.max_tokens, K = L->w.K;
-  if (T <= kSmallTokens) return MOE_OK;
+  if (T <= kExactTokens) return MOE_OK;
   L->x16 = ws;
   L->x_f = reinterpret_cast<float*>(static_cast<char*>(ws) + (((size_t)T * K * 2 + 255) & ~(size_t)255));
   PFN_cuTensorMapEncodeTiled_v12000 enc = tmap_encode_fn();
@@ -490,23 +642,53 @@ moe_status gemm_init(moe_linear* L, void* ws) {
   for (int i = 0; i < 16; ++i) {
     cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)T};
     cuuint64_t strides[1] = {(cuuint64_t)K * 2};
-    cuuint32_t box[2] = {kStepK, (cuuint32_t)(16 * (i + 1))};
+    cuuint32_t box[2] = {64, (cuuint32_t)(16 * (i + 1))};
     cuuint32_t es[2] = {1, 1};
     CUresult r = enc(&L->xmap[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, L->x16, dims, strides, box, es,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   }
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-  if (attr != cudaSuccess) return cuda_fail(attr, "gemm shared memory");
+  {
+    cuuint64_t dims[2] = {(cuuint64_t)L->w.kc * (kTileBytes / 8), (cuuint64_t)L->w.nt};
+    cuuint64_t strides[1] = {(cuuint64_t)L->w.kc * kTileBytes};
+    cuuint32_t box[2] = {kTileBytes / 8, kRowTiles};
+    cuuint32_t es[2] = {1, 1};
+    CUresult r = enc(&L->wmap, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, const_cast<uint8_t*>(L->w.tiles), dims, strides, box,
+                     es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  }
+  cudaError_t e = cudaSuccess;
+  for (auto k : {gemm_kernel<8, false>, gemm_kernel<16, false>, gemm_kernel<16, true>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  // the same split between shared memory and L1 as the GEMM's: an SM has to
+  // drain before it can change it
+  for (auto k : {prep_kernel<false, 1>, prep_kernel<false, 4>, prep_kernel<true, 1>, prep_kernel<true, 4>})
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  L->slots[0] = L->num_sms;
+  for (int i = 1; i < 4 && e == cudaSuccess; ++i) {
+    cudaLaunchConfig_t c = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 1 << i;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    c.gridDim = dim3(1 << i);
+    c.blockDim = dim3(threads(16));
+    c.dynamicSmemBytes = kMaxSmem;
+    c.attrs = at;
+    c.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&L->slots[i], gemm_kernel<16, true>, &c);
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "gemm configuration");
   return MOE_OK;
 }
 
 moe_status launch_gemm(moe_linear* L, const XIn& in, int T, uint16_t* y, cudaStream_t s) {
-  cudaError_t e = in.x ? launch_prep<false>(L, in, T, s) : launch_prep<true>(L, in, T, s);
+  const Plan pl = plan(L->w.N, L->w.kc, T, L->slots);
+  cudaError_t e = in.x ? launch_prep<false>(L, in, T, pl.ts, s) : launch_prep<true>(L, in, T, pl.ts, s);
   if (e != cudaSuccess) return cuda_fail(e, "linear prep launch");
-  const Plan pl = plan(L->w.N, L->w.kc, T, L->num_sms);
   GemmParams p = {};
   p.w = L->w;
   p.x_f = L->x_f;
@@ -517,13 +699,14 @@ moe_status launch_gemm(moe_linear* L, const XIn& in, int T, uint16_t* y, cudaStr
   p.units = pl.units;
   p.split = pl.split;
   p.stages = pl.stages;
+  p.ring = pl.ring;
   p.tmem_cols = pl.tmem_cols;
   p.err = L->err;
   p.timeout_ns = wait_timeout_ns();
   prof::Scope scope("linear_gemm", s);
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(pl.split > 1 ? pl.units * pl.split : std::min(pl.units, L->num_sms));
-  c.blockDim = dim3(kThreads);
+  c.blockDim = dim3(threads(pl.prod));
   c.dynamicSmemBytes = pl.smem;
   c.stream = s;
   cudaLaunchAttribute at[2];
@@ -534,7 +717,9 @@ moe_status launch_gemm(moe_linear* L, const XIn& in, int T, uint16_t* y, cudaStr
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   c.attrs = at;
   c.numAttrs = 2;
-  e = cudaLaunchKernelEx(&c, gemm_kernel, p, L->xmap[pl.bn / 16 - 1]);
+  auto kernel = pl.ts ? gemm_kernel<16, true> : pl.prod == 16 ? gemm_kernel<16, false> : gemm_kernel<8, false>;
+  e = cudaLaunchKernelEx(&c, kernel, p, L->xmap[pl.bn / 16 - 1],
+                         L->wmap);
   if (e != cudaSuccess) return cuda_fail(e, "linear gemm launch");
   return MOE_OK;
 }

@@ -19,29 +19,35 @@ def product(x64, w64, bias=None):
     return y if bias is None else y + bias.double()
 
 
-SMALL_TOKENS = 32  # largest batch that keeps every bit of x and W
+EXACT_TOKENS = 8  # largest batch whose weights are never rounded
+DOT_TOKENS = 2    # largest batch whose bf16 x may be taken as integers per block of 32
 
 
-def product_bound(x64, w64, y64, bias=None, tokens=1):
-    """Largest error of a bf16 y in a call on `tokens` tokens.
+def product_bound(x64, w64, y64, bias=None, tokens=1, bf16=True):
+    """Largest error of a bf16 y in a call on `tokens` tokens of bf16 (or 8-bit) x.
 
     fp32 accumulation: the products of a 32-input block are summed apart, then
     the K/32 block sums; each addition is off by at most 2^-22 of the sum of
     magnitudes (the tensor cores truncate: twice fp32's step 2^-23), a few more
     for the scales: (32 + K/32 + 8) 2^-22 of sum |x||w|.  (One long chain on the
     tensor cores adds 16 products at a time, K/16 additions: K/16 2^-22.)
-    Above SMALL_TOKENS the operands are fp16: each weight is rounded once, 2^-11
-    of itself, or, below 2^-14 in units where the row's largest scale is at
-    least 2^-6, twice by 2^-25, so 2^-18 of the row's largest scale, which is at
-    most its largest weight or, if the codes of that block are all 8 (weight 0),
-    any: 2^-17 of the row's largest |weight| is allowed for.  x loses what lies
-    below 2^-25 of the token's largest |x|.  Then half a bf16 step of the result."""
+    Up to DOT_TOKENS bf16 tokens: x as multiples of 2^(e - 13), with 2^e at most
+    the largest |x| of the block: off by 2^-14 of that at most.
+    Above EXACT_TOKENS the operands may be fp16: each weight is rounded once,
+    2^-11 of itself, or, below 2^-14 in units where the row's largest scale is
+    at least 2^-9, twice by 2^-25, so 2^-15 of the row's largest scale, which is
+    at most its largest |weight| where that block has a code other than 8.
+    x loses what lies below 2^-25 of the token's largest |x|.
+    Then half a bf16 step of the result."""
     K = x64.shape[1]
     ax, aw = x64.abs(), w64.abs()
     mag = ax @ aw.T + (0 if bias is None else bias.double().abs())
     err = mag * ((32 + K / 16 + 8) * 2.0 ** -22)
-    if tokens > SMALL_TOKENS:
-        err = err + 2.0 ** -11 * mag + 2.0 ** -17 * ax.sum(1, keepdim=True) * aw.amax(1)
+    if bf16 and tokens <= DOT_TOKENS:
+        top = ax.view(-1, K // 32, 32).amax(-1).repeat_interleave(32, 1)
+        err = err + 2.0 ** -14 * (top @ aw.T)
+    if tokens > EXACT_TOKENS:
+        err = err + 2.0 ** -11 * mag + 2.0 ** -15 * ax.sum(1, keepdim=True) * aw.amax(1)
         err = err + 2.0 ** -25 * ax.amax(1, keepdim=True) * aw.sum(1)
     return err + (y64.abs() + err) * 2.0 ** -8 + 1e-38
 

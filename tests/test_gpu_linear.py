@@ -20,14 +20,14 @@ def acts(T, K, seed=0):
     return (torch.randn(T, K, generator=g) * torch.exp(torch.randn(T, 1, generator=g))).bfloat16()
 
 
-def check(y, x64, w64, bias, tokens=None):
+def check(y, x64, w64, bias, tokens=None, bf16=True):
     y64 = R.product(x64, w64, bias)
     off = (y.double().cpu() - y64).abs()
-    bound = R.product_bound(x64, w64, y64, bias, tokens or x64.shape[0])
+    bound = R.product_bound(x64, w64, y64, bias, tokens or x64.shape[0], bf16)
     assert (off <= bound).all(), (off / bound).max().item()
 
 
-SMALL = [(1, 16, 32), (1, 1, 32), (1, 17, 64), (1, 2048, 2048), (2, 100, 96), (3, 2049, 160), (4, 33, 8192), (5, 640, 1056),
+SMALL = [(1, 16, 32), (2, 16, 32), (4, 30, 32), (1, 50, 16384), (1, 30, 32768), (2, 3000, 10272), (3, 700, 2048), (1, 1, 32), (1, 17, 64), (1, 2048, 2048), (2, 100, 96), (3, 2049, 160), (4, 33, 8192), (5, 640, 1056),
          (8, 257, 2080), (9, 1000, 256), (16, 4099, 512), (17, 48, 2048), (31, 515, 1024), (32, 1024, 4096),
          (1, 40000, 256), (8, 5000, 4128), (32, 16, 32768), (24, 9000, 128)]
 
@@ -49,10 +49,10 @@ def test_q8(cuda_device, T, N, K):
     q = torch.randint(-127, 128, (T, K), generator=g).to(torch.int8)
     s = torch.rand(T, K // 32, generator=g) + 0.01
     y = lin.forward_q8(q.to(cuda_device), s.to(cuda_device))
-    check(y, R.q8_values(q, s), w, b)
+    check(y, R.q8_values(q, s), w, b, bf16=False)
 
 
-LARGE = [(33, 100, 64), (40, 2048, 2048), (64, 300, 96), (65, 1, 32), (100, 4111, 2080), (128, 128, 128),
+LARGE = [(9, 30000, 2048), (17, 30, 64), (16, 24000, 2080), (33, 100, 64), (40, 2048, 2048), (64, 300, 96), (65, 1, 32), (100, 4111, 2080), (128, 128, 128),
          (129, 513, 1056), (200, 777, 4096), (256, 256, 256), (257, 1025, 544), (511, 48, 8192), (700, 2560, 2048),
          (1025, 640, 160), (2050, 2050, 320), (65, 20000, 64), (40, 70000, 32), (48, 130, 32768), (5000, 1300, 96)]
 

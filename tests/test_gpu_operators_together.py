@@ -74,7 +74,7 @@ def test_block(cuda_device, model, T):
                           atol=0)
     x64 = R.q8_values(u2[0].cpu(), u2[1].cpu()) if T <= 32 else u2.cpu().double()
     y64 = R.product(x64, w1)
-    assert ((logits.cpu().double() - y64).abs() <= R.product_bound(x64, w1, y64, None, T)).all()
+    assert ((logits.cpu().double() - y64).abs() <= R.product_bound(x64, w1, y64, None, T, T > 32)).all()
 
 
 @pytest.mark.parametrize("T", [1, 40])
