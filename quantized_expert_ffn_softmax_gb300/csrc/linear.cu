@@ -58,7 +58,7 @@ __global__ void pack_kernel(const uint8_t* __restrict__ q, const uint16_t* __res
   for (int half = 0; half < 2; ++half) {
     uint32_t w[4];
     for (int i = 0; i < 4; ++i) {
-      const int row = row0 + frag_row(g) + 8 * (i & 1), k = k0 + 64 * half + 32 * (i >> 1) + 8 * t;
+      const int row = row0 + g + 8 * (i & 1), k = k0 + 64 * half + 32 * (i >> 1) + 8 * t;
       uint32_t v = 0x88888888u;  // code 8: weight 0
       if (row < N && k < K) {
         const uint8_t* b = q + (size_t)row * (K / 2) + k / 2;  // four bytes: inputs k .. k + 7
@@ -69,8 +69,8 @@ __global__ void pack_kernel(const uint8_t* __restrict__ q, const uint16_t* __res
     }
     *reinterpret_cast<uint4*>(dst + 512 * half + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  for (int i = lane; i < 64; i += 32) {  // scale i: fragment row i / 8, then block
-    const int row = row0 + frag_row(i >> 3) + 8 * ((i >> 2) & 1), blk = k0 / 32 + (i & 3);
+  for (int i = lane; i < 64; i += 32) {  // scale i: rows i / 8 and + 8, then block
+    const int row = row0 + (i >> 3) + 8 * ((i >> 2) & 1), blk = k0 / 32 + (i & 3);
     uint16_t v = 0;
     if (row < N && blk < K / 32)
       v = __half_as_ushort(__float2half_rn(__half2float(__ushort_as_half(s[(size_t)row * (K / 32) + blk])) / row_f[row]));
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(256, kCtas) dot_kernel(const __grid_constant__
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int row = (unit * MT + m) * kTileRows + frag_row(g) + 8 * r;
+          const int row = (unit * MT + m) * kTileRows + g + 8 * r;
           if (row < p.w.N) {
             const float rf = __ldg(p.w.row_f + row), bias = p.w.bias ? __ldg(p.w.bias + row) : 0.0f;
 #pragma unroll
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(256, kCtas) small_kernel(const __grid_constant
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int row = (unit * MT + m) * kTileRows + frag_row(g) + 8 * h;
+          const int row = (unit * MT + m) * kTileRows + g + 8 * h;
           if (row < p.w.N) {
             const float rf = __ldg(p.w.row_f + row), bias = p.w.bias ? __ldg(p.w.bias + row) : 0.0f;
 #pragma unroll

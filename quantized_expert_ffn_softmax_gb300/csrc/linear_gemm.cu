@@ -13,20 +13,27 @@
 // which is how the scales are stored, or s' * 2^20, and -8 s' gives the weight
 // with a single rounding and without a conversion.
 //
-// Operand A (the weights) goes through tensor memory for tiles of up to 128
-// tokens (kTs) and through shared memory above: read from shared memory an MMA
-// takes about 110 cycles however few its tokens (897 cycles for the 8 of a
-// stage at 16 to 64 tokens), from tensor memory its time falls with N; but
-// tensor memory holds A stages beside two accumulators only up to 128 tokens.
+// Operand A (the weights) goes through tensor memory: read from shared memory
+// an MMA takes about 110 cycles however few its tokens (897 cycles for the 8 of
+// a stage at 16 to 64 tokens), and at 256 tokens shared memory would have to
+// move 192 bytes a cycle of its 128.  Two accumulators and the A stages share
+// the 512 columns: 4 stages up to 128 tokens a tile, 2 at 192, the most.
 //
 // One CTA per SM, warp-specialised, 128 inputs per stage.  Warps 0-7:
-// epilogue (two per TMEM lane quarter, taking turns by 16 tokens).  Then 8 or
-// 16 producers: each turns its 16 rows of a packed tile into fp16 rows of the
-// stage's A tile; 16 take turns by stage.  Then
-// one warp each for the TMA of the packed tiles (8 row tiles in one copy, into
-// a ring), the TMA of the x16 tile and the MMAs.  Few row blocks: S CTAs of a cluster share one output tile, each
-// with a part of K, and sum their fp32 tiles through distributed shared
-// memory in rank order.
+// epilogue (two per TMEM lane quarter, taking turns by 16 tokens).  Then 16
+// producers: four turn a packed tile into the stage's A tile, 32 rows each, and
+// the groups of four take turns by stage.  Then one warp each for the TMA of
+// the packed tiles (8 row tiles in one copy, into a ring), the TMA of the x16
+// tile and the MMAs.  Few row blocks: S CTAs of a cluster share one output
+// tile, each with a part of K, and sum their fp32 tiles through distributed
+// shared memory in rank order.
+//
+// Turns.  A group waits for phases by parity, so it must never be two phases
+// behind: its next stage is `turns` further, the phase it waits for there is
+// the commit of the tile `stages` before that, and it knows (commits are in
+// order) the commit of the tile `stages` before its last one; so turns <=
+// stages.  In the packed ring the copy `ring` tiles earlier must be known to
+// have landed: ring >= stages + turns.
 #include <string.h>
 
 #include <algorithm>
@@ -44,24 +51,27 @@ using namespace dev;
 using namespace op;
 
 constexpr int kRowsA = 128;               // rows of W per tile
-constexpr int kHalfA = kRowsA * 128;      // bytes of 64 inputs of the A tile
-constexpr int kABytes = 2 * kHalfA;       // A tile of a stage (128 inputs)
+constexpr int kACols = 64;                // TMEM columns of an A stage (128 inputs)
+constexpr int kMaxTile = 192;             // tokens per tile
 constexpr int kRowTiles = kRowsA / kTileRows;  // 8: producers per stage
 constexpr int kMaxStages = 6;
-constexpr int kTsTokens = 128;                 // largest tile with A in tensor memory
 constexpr int kBarBytes = 512;
-constexpr int kXfBytes = 256 * 4;
+constexpr int kXfBytes = kMaxTile * 4;
 constexpr int kMaxSmem = 227 * 1024;
 constexpr int kEpiWarps = 8;
 constexpr int kRaw = kRowTiles * kTileBytes;   // packed weights of a stage
 constexpr int kMaxRing = 16;
-constexpr int threads(int prod) { return (kEpiWarps + prod + 3) * 32; }
+constexpr int kProdWarps = 16;
+constexpr int kStageProds = 4;                 // producers of a stage: 32 rows each
+constexpr int kMaxTurns = kProdWarps / kStageProds;
+constexpr int kProd0 = kEpiWarps, kRawWarp = kProd0 + kProdWarps, kLoadWarp = kRawWarp + 1, kMmaWarp = kLoadWarp + 1;
+constexpr int kThreads = (kMmaWarp + 1) * 32;
 
 // ------------------------------------------------------------ prep
-// perm: inside every block of 32 inputs, pair i of the 8 inputs 8 t .. 8 t + 7
-// goes to pair 4 i + t, the order in which A fragments lie in tensor memory.
+// Inside every block of 32 inputs, pair i of the 8 inputs 8 t .. 8 t + 7 goes
+// to pair 4 i + t, the order in which A fragments lie in tensor memory.
 template <bool kQ8, int V>
-__global__ void __launch_bounds__(1024) prep_kernel(const XIn in, int K, bool perm, __half* __restrict__ x16,
+__global__ void __launch_bounds__(1024) prep_kernel(const XIn in, int K, __half* __restrict__ x16,
                                                     float* __restrict__ x_f) {
   __shared__ uint32_t red[32];
   dep_wait();
@@ -107,13 +117,9 @@ __global__ void __launch_bounds__(1024) prep_kernel(const XIn in, int K, bool pe
       __half2 h[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) h[k] = __floats2half2_rn(v[j][2 * k] * f, v[j][2 * k + 1] * f);
-      if (perm) {
-        __half2* o = reinterpret_cast<__half2*>(x16 + (size_t)t * K + 32 * (i >> 2)) + (i & 3);
+      __half2* o = reinterpret_cast<__half2*>(x16 + (size_t)t * K + 32 * (i >> 2)) + (i & 3);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[4 * k] = h[k];
-      } else {
-        *reinterpret_cast<uint4*>(x16 + (size_t)t * K + 8 * i) = *reinterpret_cast<const uint4*>(h);
-      }
+      for (int k = 0; k < 4; ++k) o[4 * k] = h[k];
     }
   }
   if (threadIdx.x == 0) x_f[t] = pow2f(e);
@@ -125,13 +131,13 @@ struct GemmParams {
   const float* x_f;
   uint16_t* y;
   int T;
-  int bn;        // tokens per tile: a multiple of 16, 16 .. 256
+  int bn;        // tokens per tile: a multiple of 16, 16 .. kMaxTile
   int n_rb;      // row blocks
   int units;     // row blocks x token tiles
   int split;     // CTAs of a cluster that share a unit (1: units are walked persistently)
   int stages;
   int ring;
-  int tmem_cols;
+  int turns;     // producer groups in use
   int* err;
   unsigned long long timeout_ns;
 };
@@ -210,23 +216,18 @@ __device__ __forceinline__ void tmem_st_16x128b_x16(uint32_t taddr, const uint32
       : "memory");
 }
 
-// kProd: producer warps (8 or 16).  kTs: operand A in tensor memory.
-template <int kProd, bool kTs>
-__global__ void __launch_bounds__(threads(kProd), 1)
+__global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ GemmParams p, const __grid_constant__ CUtensorMap xmap,
                 const __grid_constant__ CUtensorMap wmap) {
-  constexpr int kProd0 = kEpiWarps, kRawWarp = kProd0 + kProd, kLoadWarp = kRawWarp + 1, kMmaWarp = kLoadWarp + 1;
-  constexpr int kTurns = kProd / kRowTiles;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                          ~static_cast<uintptr_t>(1023));
   const int bn = p.bn, S = p.stages;
-  constexpr int kA = kTs ? 0 : kABytes;  // bytes of A in a stage
-  const int half_b = bn * 128, stage_bytes = kA + 2 * half_b;
+  const int half_b = bn * 128, stage_bytes = 2 * half_b;  // the x16 tile
   const int R = p.ring;
   unsigned char* raw = smem + S * stage_bytes;  // R packed tiles of 128 rows x 128 inputs
-  float* xf = reinterpret_cast<float*>(raw + R * kRaw);  // [256] token factors
-  uint64_t* full = reinterpret_cast<uint64_t*>(xf + 256);
+  float* xf = reinterpret_cast<float*>(raw + R * kRaw);  // [kMaxTile] token factors
+  uint64_t* full = reinterpret_cast<uint64_t*>(xf + kMaxTile);
   uint64_t* empty = full + kMaxStages;
   uint64_t* raw_full = empty + kMaxStages;
   uint64_t* raw_empty = raw_full + kMaxRing;
@@ -238,12 +239,12 @@ __global__ void __launch_bounds__(threads(kProd), 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], kRowTiles + 1);  // + the loader's arrive with the tile's bytes
+      mbar_init(&full[s], kStageProds + 1);  // + the loader's arrive with the tile's bytes
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < R; ++s) {
       mbar_init(&raw_full[s], 1);
-      mbar_init(&raw_empty[s], kRowTiles);
+      mbar_init(&raw_empty[s], kStageProds);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(threads(kProd), 1)
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(tmem_slot, p.tmem_cols);
+    tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -275,13 +276,11 @@ __global__ void __launch_bounds__(threads(kProd), 1)
     // quarter take alternate groups of 16 tokens.
     dep_wait();
     dep_release();
-    // With A in tensor memory lane 16 w + g holds the row of fragment row g.
     const int r = (warp & 3) * 32 + lane, c_first = 16 * (warp >> 2);
-    const int rr = kTs ? (r & ~7) + frag_row(r & 7) : r;
-    const size_t N = p.w.N;
+        const size_t N = p.w.N;
     int j = 0;
     for (int u = u0; u < p.units; u += ustep, ++j) {
-      const int row = (u % p.n_rb) * kRowsA + rr, t0 = (u / p.n_rb) * bn;
+      const int row = (u % p.n_rb) * kRowsA + r, t0 = (u / p.n_rb) * bn;
       const int nt = min(bn, p.T - t0);
       const int b = j & 1;
       // token factors of the tile (the warps agree on going on: the named
@@ -329,7 +328,7 @@ __global__ void __launch_bounds__(threads(kProd), 1)
           tmem_ld16(tb + c, v);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) part[(c + i) * kRowsA + rr] = __uint_as_float(v[i]);
+          for (int i = 0; i < 16; ++i) part[(c + i) * kRowsA + r] = __uint_as_float(v[i]);
         }
       }
       tc_fence_before();
@@ -339,64 +338,52 @@ __global__ void __launch_bounds__(threads(kProd), 1)
     // ------------------------------------------------------------ producers
     dep_wait();
     dep_release();
-    // The row tile: any, or with A in tensor memory one of the two whose lanes
-    // the warp can reach.
-    const int pw = warp - kProd0, g = lane >> 2, t = lane & 3;
-    const int w = kTs ? 2 * (warp & 3) + ((pw >> 2) & 1) : pw & (kRowTiles - 1), turn = pw / kRowTiles;
-    // ring slot and stage of every kTurns-th packed tile, with the parities of
+    // A warp turns the 32 rows (two row tiles) of its TMEM lane quarter; four
+    // warps make a stage, the sixteen take turns.
+    const int q = warp & 3, turn = (warp - kProd0) / kStageProds, g = lane >> 2;
+    // ring slot and stage of every turns-th packed tile, with the parities of
     // the phases to wait for
     int slot = turn, st = turn;
     uint32_t rpar = 0, par = 1;
-    // rows frag_row(g) and + 8 of the warp's 16, 16-byte chunk 4 b + t of 64
-    // inputs for block b, XOR-swizzled by the row
-    const int fr = frag_row(g);
-    const uint32_t o0 = (uint32_t)((16 * w + fr) * 128 + (t ^ fr) * 16), o1 = o0 ^ 64;
-    const unsigned char* mine = raw + w * kTileBytes;
-    for (int i = turn; i < total; i += kTurns) {
+    const unsigned char* mine = raw + 2 * q * kTileBytes;
+    const int n_tiles = turn < p.turns ? total : 0;  // (a group too many has nothing to do)
+    for (int i = turn; i < n_tiles; i += p.turns) {
       if (!__all_sync(0xffffffffu, mbar_wait(&raw_full[slot], rpar, p.err, tmo))) break;
-      const unsigned char* tl = mine + slot * kRaw;
-      const uint4 w0 = *reinterpret_cast<const uint4*>(tl + 16 * lane);
-      const uint4 w1 = *reinterpret_cast<const uint4*>(tl + 512 + 16 * lane);
-      const uint4 sc = *reinterpret_cast<const uint4*>(tl + kTileCodes + 16 * g);
-      // row frag_row(g) (even) and + 8 (odd) of block 0 .. 3: pair i of block b
-      // at o[8 b + 2 i] and o[8 b + 2 i + 1], its column 16 b + 4 i + t
-      uint32_t o[32];
-      auto put = [&](int b, uint32_t wa, uint32_t wb, uint32_t q, int row) {
-        uint4 da, db;
-        dequant16(wa, wb, q, da, db);
-        uint32_t* d = o + 8 * b + row;
-        d[0] = da.x, d[2] = da.y, d[4] = da.z, d[6] = da.w;
-        d[8] = db.x, d[10] = db.y, d[12] = db.z, d[14] = db.w;
-      };
-      put(0, w0.x, w0.z, sc.x, 0);
-      put(0, w0.y, w0.w, sc.z, 1);
-      put(2, w1.x, w1.z, sc.y, 0);
-      put(2, w1.y, w1.w, sc.w, 1);
-      // the ring slot's reads come before the next copy into it
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&raw_empty[slot]);
-      slot += kTurns;
-      if (slot >= R) slot -= R, rpar ^= 1;
       if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], par, p.err, tmo))) break;
-      if constexpr (kTs) {
-        tc_fence_after();
-        tmem_st_16x128b_x16(tmem + ((uint32_t)(16 * w) << 16) + (uint32_t)(2 * bn + 64 * st), o);
-        tmem_wait_st();
-        tc_fence_before();
-      } else {
-        unsigned char* A = smem + st * stage_bytes;
+      tc_fence_after();
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          unsigned char* d = A + (b >> 1) * kHalfA + ((b & 1) ? o1 : o0);
-          *reinterpret_cast<uint4*>(d) = make_uint4(o[8 * b], o[8 * b + 2], o[8 * b + 4], o[8 * b + 6]);
-          *reinterpret_cast<uint4*>(d + 1024) = make_uint4(o[8 * b + 1], o[8 * b + 3], o[8 * b + 5], o[8 * b + 7]);
-        }
-        fence_proxy_async_smem();  // the writes before the MMA's reads
+      for (int h = 0; h < 2; ++h) {  // row tile 2 q + h
+        const unsigned char* tl = mine + slot * kRaw + h * kTileBytes;
+        const uint4 w0 = *reinterpret_cast<const uint4*>(tl + 16 * lane);
+        const uint4 w1 = *reinterpret_cast<const uint4*>(tl + 512 + 16 * lane);
+        const uint4 sc = *reinterpret_cast<const uint4*>(tl + kTileCodes + 16 * g);
+        // row g (even) and + 8 (odd) of block 0 .. 3: pair i of block
+        // b at o[8 b + 2 i] and o[8 b + 2 i + 1], its column 16 b + 4 i + t
+        uint32_t o[32];
+        auto put = [&](int b, uint32_t wa, uint32_t wb, uint32_t s2, int row) {
+          uint4 da, db;
+          dequant16(wa, wb, s2, da, db);
+          uint32_t* d = o + 8 * b + row;
+          d[0] = da.x, d[2] = da.y, d[4] = da.z, d[6] = da.w;
+          d[8] = db.x, d[10] = db.y, d[12] = db.z, d[14] = db.w;
+        };
+        put(0, w0.x, w0.z, sc.x, 0);
+        put(0, w0.y, w0.w, sc.z, 1);
+        put(2, w1.x, w1.z, sc.y, 0);
+        put(2, w1.y, w1.w, sc.w, 1);
+        tmem_st_16x128b_x16(tmem + ((uint32_t)(32 * q + 16 * h) << 16) + (uint32_t)(2 * bn + kACols * st), o);
       }
+      fence_proxy_async_smem();  // the ring slot's reads come before the next copy into it
+      tmem_wait_st();
+      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&full[st]);
-      st += kTurns;
+      if (lane == 0) {
+        mbar_arrive(&full[st]);
+        mbar_arrive(&raw_empty[slot]);
+      }
+      slot += p.turns;
+      if (slot >= R) slot -= R, rpar ^= 1;
+      st += p.turns;
       if (st >= S) st -= S, par ^= 1;
     }
   } else if (warp == kRawWarp) {
@@ -442,7 +429,7 @@ __global__ void __launch_bounds__(threads(kProd), 1)
           break;
         }
         if (elect_one()) {
-          unsigned char* B = smem + st * stage_bytes + kA;
+          unsigned char* B = smem + st * stage_bytes;
           mbar_expect_tx(&full[st], (uint32_t)(2 * half_b));
           tma_load_2d(B, &xmap, c * kTileK, t0, &full[st]);
           tma_load_2d(B + half_b, &xmap, c * kTileK + 64, t0, &full[st]);  // past K: zeros
@@ -460,8 +447,8 @@ __global__ void __launch_bounds__(threads(kProd), 1)
     // two stages' MMAs are what leaves the tensor core idle on small tiles.
     const uint32_t idesc = idesc_f16_m128(bn);
     const uint64_t d0 = smem_desc_sw128(smem_u32(smem));
-    const uint64_t a1 = kHalfA >> 4, b0 = kA >> 4, b1 = b0 + (half_b >> 4), dstep = stage_bytes >> 4;
-    uint64_t da = d0;
+    const uint64_t half = half_b >> 4, dstep = stage_bytes >> 4;
+    uint64_t db = d0;
     int st = 0, j = 0;
     uint32_t par = 0;
     for (int u = u0; u < p.units; u += ustep, ++j) {
@@ -478,26 +465,18 @@ __global__ void __launch_bounds__(threads(kProd), 1)
         }
         tc_fence_after();
         if (elect_one()) {
-          if constexpr (kTs) {
-            const uint32_t a = tmem + (uint32_t)(2 * bn + 64 * st);  // 16 inputs: 8 columns
-            umma_f16_ts(d, a, da, idesc, acc);
+          const uint32_t a = tmem + (uint32_t)(2 * bn + kACols * st);  // 16 inputs: 8 columns
+          umma_f16_ts(d, a, db, idesc, acc);
 #pragma unroll
-            for (int k = 1; k < 4; ++k) umma_f16_ts(d, a + 8 * k, da + 2 * k, idesc, 1u);
+          for (int k = 1; k < 4; ++k) umma_f16_ts(d, a + 8 * k, db + 2 * k, idesc, 1u);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) umma_f16_ts(d, a + 32 + 8 * k, da + b1 + 2 * k, idesc, 1u);
-          } else {
-            umma_f16(d, da, da + b0, idesc, acc);
-#pragma unroll
-            for (int k = 1; k < 4; ++k) umma_f16(d, da + 2 * k, da + b0 + 2 * k, idesc, 1u);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) umma_f16(d, da + a1 + 2 * k, da + b1 + 2 * k, idesc, 1u);
-          }
+          for (int k = 0; k < 4; ++k) umma_f16_ts(d, a + 32 + 8 * k, db + half + 2 * k, idesc, 1u);
           umma_commit(&empty[st]);
         }
         __syncwarp();
         acc = 1;
-        da += dstep;
-        if (++st == S) st = 0, par ^= 1, da = d0;
+        db += dstep;
+        if (++st == S) st = 0, par ^= 1, db = d0;
       }
       if (!ok) break;
       if (elect_one()) umma_commit(&tfull[b]);
@@ -545,28 +524,26 @@ __global__ void __launch_bounds__(threads(kProd), 1)
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, p.tmem_cols);
+    tmem_dealloc(tmem, 512);
   }
 }
 
 // Shape of a launch.
 struct Plan {
-  bool ts;
-  int bn, units, split, prod, stages, ring, smem, tmem_cols;
+  int bn, units, split, stages, ring, turns, smem;
 };
 
 // slots[i]: clusters of 2^i CTAs that run at once (an SM holds one CTA; GPCs
 // whose SM count is no multiple leave some out: 16 clusters of 8 do not fit).
 // Tokens per tile and CTAs per tile, by an estimate of the time in cycles:
-// a step of 64 inputs takes 2 cycles per token on the tensor core (440 at
-// least with A in shared memory) and about 200 in the producers, whichever is
-// longer; 2500 cycles per tile for its start and epilogue, 1500 more for the
-// sum over a cluster.
+// a step of 64 inputs takes 2 cycles per token on the tensor core and about
+// 200 in the producers, whichever is longer; 2500 cycles per tile for its
+// start and epilogue, 1500 more for the sum over a cluster.
 Plan plan(int N, int kc, int T, const int (&slots)[4]) {
   Plan best = {};
   double best_t = 0.0;
   const int rb = (N + kRowsA - 1) / kRowsA;
-  const int j0 = (T + 255) / 256;
+  const int j0 = (T + kMaxTile - 1) / kMaxTile;
   for (int j = j0; j <= j0 + 8; ++j) {
     const int bn = ((T + j - 1) / j + 15) / 16 * 16;
     if (j > j0 && bn < 32) break;
@@ -578,7 +555,7 @@ Plan plan(int N, int kc, int T, const int (&slots)[4]) {
       if (i && units > slots[i]) break;
       const int rounds = (units + slots[i] - 1) / slots[i];
       const double steps = 2.0 * ((kc + split - 1) / split);
-      const double t = rounds * (steps * std::max(2 * bn, bn > kTsTokens ? 440 : 200) + 2500) + (split > 1 ? 1500 : 0);
+      const double t = rounds * (steps * std::max(2 * bn, 200) + 2500) + (split > 1 ? 1500 : 0);
       if (best_t == 0.0 || t < best_t) {
         best_t = t;
         best.bn = bn;
@@ -587,41 +564,32 @@ Plan plan(int N, int kc, int T, const int (&slots)[4]) {
       }
     }
   }
-  const int room = kMaxSmem - 1024 - kBarBytes - kXfBytes;
-  best.ts = best.bn <= kTsTokens;
-  best.tmem_cols = 512;
-  if (best.ts) {
-    const int stage = best.bn * 256;
-    best.prod = 16;
-    best.stages = std::min(kMaxStages, (512 - 2 * best.bn) / 64);
-    best.ring = std::min(kMaxRing, (room - best.stages * stage) / kRaw);
-    best.smem = best.stages * stage;
-  } else {
-    const int stage = kABytes + best.bn * 256;
-    // 16 producers where three stages fit beside a deep ring; else 8, whose
-    // rate is enough there (a stage then has 190 or more tokens of MMA work)
-    best.prod = room - 6 * kRaw >= 3 * stage ? 16 : 8;
-    best.ring = best.prod == 16 ? 6 : 3;
-    best.stages = std::min(kMaxStages, (room - best.ring * kRaw) / stage);
-    best.smem = best.stages * stage;
-  }
-  best.smem += best.ring * kRaw + kBarBytes + kXfBytes + 1024;
+  const int room = kMaxSmem - 1024 - kBarBytes - kXfBytes, stage = best.bn * 256;
+  best.stages = std::min(kMaxStages, (512 - 2 * best.bn) / kACols);
+  best.turns = std::min(kMaxTurns, best.stages);
+  best.ring = std::min(kMaxRing, (room - best.stages * stage) / kRaw);  // >= stages + turns, see below
+  best.smem = best.stages * stage + best.ring * kRaw + kBarBytes + kXfBytes + 1024;
   return best;
 }
-static_assert(2 * (kABytes + 256 * 256) + 3 * kRaw + kBarBytes + kXfBytes + 1024 <= kMaxSmem,
-              "two stages at 256 tokens");
-// two stages hold the fp32 tile of a shared unit: 2 (kABytes + 256 bn) >= 512 bn
+constexpr int ring_at(int bn, int stages) {
+  return (kMaxSmem - 1024 - kBarBytes - kXfBytes - stages * bn * 256) / kRaw;
+}
+static_assert(ring_at(192, 2) >= 4 && ring_at(160, 3) >= 6 && ring_at(128, 4) >= 8 && ring_at(96, 5) >= 9 &&
+                  ring_at(64, 6) >= 10 && kMaxRing >= kMaxStages + kMaxTurns,
+              "ring >= stages + turns at the largest tile of every stage count");
+// the stages hold the fp32 tile of a shared unit: stages * 256 bn >= 512 bn
+static_assert((512 - 2 * kMaxTile) / kACols >= 2, "two stages");
 static_assert(8 * (2 * kMaxStages + 2 * kMaxRing + 5) + 4 <= kBarBytes, "barriers");
 
 template <bool kQ8>
-cudaError_t launch_prep(moe_linear* L, const XIn& in, int T, bool perm, cudaStream_t s) {
+cudaError_t launch_prep(moe_linear* L, const XIn& in, int T, cudaStream_t s) {
   prof::Scope scope(kQ8 ? "linear_prep_q8" : "linear_prep", s);
   const int nvec = L->w.K / 8;
   __half* x16 = static_cast<__half*>(L->x16);
   if (nvec <= 1024)
-    return launch_overlapped(prep_kernel<kQ8, 1>, dim3(T), dim3((nvec + 31) / 32 * 32), 0, s, in, L->w.K, perm, x16,
+    return launch_overlapped(prep_kernel<kQ8, 1>, dim3(T), dim3((nvec + 31) / 32 * 32), 0, s, in, L->w.K, x16,
                              L->x_f);
-  return launch_overlapped(prep_kernel<kQ8, 4>, dim3(T), dim3(((nvec + 3) / 4 + 31) / 32 * 32), 0, s, in, L->w.K, perm, x16,
+  return launch_overlapped(prep_kernel<kQ8, 4>, dim3(T), dim3(((nvec + 3) / 4 + 31) / 32 * 32), 0, s, in, L->w.K, x16,
                            L->x_f);
 }
 
@@ -639,7 +607,7 @@ moe_status gemm_init(moe_linear* L, void* ws) {
   L->x_f = reinterpret_cast<float*>(static_cast<char*>(ws) + (((size_t)T * K * 2 + 255) & ~(size_t)255));
   PFN_cuTensorMapEncodeTiled_v12000 enc = tmap_encode_fn();
   if (!enc) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < kMaxTile / 16; ++i) {
     cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)T};
     cuuint64_t strides[1] = {(cuuint64_t)K * 2};
     cuuint32_t box[2] = {64, (cuuint32_t)(16 * (i + 1))};
@@ -659,9 +627,7 @@ moe_status gemm_init(moe_linear* L, void* ws) {
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   }
-  cudaError_t e = cudaSuccess;
-  for (auto k : {gemm_kernel<8, false>, gemm_kernel<16, false>, gemm_kernel<16, true>})
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  cudaError_t e = cudaFuncSetAttribute(gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   // the same split between shared memory and L1 as the GEMM's: an SM has to
   // drain before it can change it
   for (auto k : {prep_kernel<false, 1>, prep_kernel<false, 4>, prep_kernel<true, 1>, prep_kernel<true, 4>})
@@ -675,11 +641,11 @@ moe_status gemm_init(moe_linear* L, void* ws) {
     at[0].val.clusterDim.x = 1 << i;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     c.gridDim = dim3(1 << i);
-    c.blockDim = dim3(threads(16));
+    c.blockDim = dim3(kThreads);
     c.dynamicSmemBytes = kMaxSmem;
     c.attrs = at;
     c.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&L->slots[i], gemm_kernel<16, true>, &c);
+    e = cudaOccupancyMaxActiveClusters(&L->slots[i], gemm_kernel, &c);
   }
   if (e != cudaSuccess) return cuda_fail(e, "gemm configuration");
   return MOE_OK;
@@ -687,7 +653,7 @@ moe_status gemm_init(moe_linear* L, void* ws) {
 
 moe_status launch_gemm(moe_linear* L, const XIn& in, int T, uint16_t* y, cudaStream_t s) {
   const Plan pl = plan(L->w.N, L->w.kc, T, L->slots);
-  cudaError_t e = in.x ? launch_prep<false>(L, in, T, pl.ts, s) : launch_prep<true>(L, in, T, pl.ts, s);
+  cudaError_t e = in.x ? launch_prep<false>(L, in, T, s) : launch_prep<true>(L, in, T, s);
   if (e != cudaSuccess) return cuda_fail(e, "linear prep launch");
   GemmParams p = {};
   p.w = L->w;
@@ -700,13 +666,13 @@ moe_status launch_gemm(moe_linear* L, const XIn& in, int T, uint16_t* y, cudaStr
   p.split = pl.split;
   p.stages = pl.stages;
   p.ring = pl.ring;
-  p.tmem_cols = pl.tmem_cols;
+  p.turns = pl.turns;
   p.err = L->err;
   p.timeout_ns = wait_timeout_ns();
   prof::Scope scope("linear_gemm", s);
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(pl.split > 1 ? pl.units * pl.split : std::min(pl.units, L->num_sms));
-  c.blockDim = dim3(threads(pl.prod));
+  c.blockDim = dim3(kThreads);
   c.dynamicSmemBytes = pl.smem;
   c.stream = s;
   cudaLaunchAttribute at[2];
@@ -717,8 +683,7 @@ moe_status launch_gemm(moe_linear* L, const XIn& in, int T, uint16_t* y, cudaStr
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   c.attrs = at;
   c.numAttrs = 2;
-  auto kernel = pl.ts ? gemm_kernel<16, true> : pl.prod == 16 ? gemm_kernel<16, false> : gemm_kernel<8, false>;
-  e = cudaLaunchKernelEx(&c, kernel, p, L->xmap[pl.bn / 16 - 1],
+  e = cudaLaunchKernelEx(&c, gemm_kernel, p, L->xmap[pl.bn / 16 - 1],
                          L->wmap);
   if (e != cudaSuccess) return cuda_fail(e, "linear gemm launch");
   return MOE_OK;

@@ -14,21 +14,16 @@ namespace lin {
 // .. 128 c + 127 in kTileBytes bytes, tiles of one i contiguous in c:
 //   1024 B of codes: two halves of 64 inputs (two scale blocks each); in a
 //     half lane l = 4 g + t of a warp finds 16 bytes at 16 l: one word of
-//     block 0 row frag_row(g), block 0 row frag_row(g) + 8, then the same of
-//     block 1.  A word holds the inputs 8 t .. 8 t + 7 of its block: input
+//     block 0 row g, block 0 row g + 8, block 1 row g, block 1 row g + 8.  A word holds the inputs 8 t .. 8 t + 7 of its block: input
 //     2 i in nibble i and input 2 i + 1 in nibble i + 4, so that
 //     (word >> 4 i) & 0x000f000f is the pair (2 i, 2 i + 1).
-//   128 B of scales: at 16 g the four block scales of row frag_row(g), then
-//     of row frag_row(g) + 8, each times the power of two that brings the
+//   128 B of scales: at 16 g the four block scales of row g, then of row
+//     g + 8, each times the power of two that brings the
 //     largest magnitude of its row to [2^15, 2^16) (exact: that only shifts
 //     exponents up); row_f is the inverse.
-// The words are the A fragments of mma.m16n8k16 (two MMAs per scale block),
-// and eight consecutive inputs of a row in one 16-byte store of the tcgen05
-// path's shared-memory tiles, where the order of the rows puts eight
-// consecutive lanes on eight different 16-byte chunks of the 128-byte swizzle.
-// Rows past N and inputs past K have scale 0.
-__host__ __device__ constexpr int frag_row(int g) { return (g >> 1) | ((g & 1) << 2); }
-
+// The words are the A fragments of mma.m16n8k16 (two MMAs per scale block), of
+// the dot products and of the tcgen05 path's stores into tensor memory.  Rows
+// past N and inputs past K have scale 0.
 constexpr int kTileRows = 16;
 constexpr int kTileK = 128;
 constexpr int kTileCodes = 1024;
@@ -68,7 +63,7 @@ struct moe_linear {
   void* x16 = nullptr;      // [max_tokens][K] fp16 operand rows (batches above kExactTokens)
   float* x_f = nullptr;     // [max_tokens] token factors
   CUtensorMap wmap;         // packed tiles, boxes of one tile along K by 8 along N
-  CUtensorMap xmap[16];     // x16 with boxes of 64 inputs by 16 (i + 1) tokens
+  CUtensorMap xmap[12];     // x16 with boxes of 64 inputs by 16 (i + 1) tokens
   int device = 0;
   int num_sms = 0;
   int slots[4] = {};        // clusters of 1, 2, 4, 8 CTAs of the GEMM that run at once
