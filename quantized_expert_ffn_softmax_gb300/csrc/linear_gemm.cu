@@ -17,23 +17,25 @@
 // an MMA takes about 110 cycles however few its tokens (897 cycles for the 8 of
 // a stage at 16 to 64 tokens), and at 256 tokens shared memory would have to
 // move 192 bytes a cycle of its 128.  Two accumulators and the A stages share
-// the 512 columns: 4 stages up to 128 tokens a tile, 2 at 192, the most.
+// the 512 columns: 4 stages at 128 tokens a tile, 3 at 160, the most (with 2, at
+// 192 tokens, the stages wait for their copies: 8192 x 2048-8192 takes 198 us
+// against 173).
 //
 // One CTA per SM, warp-specialised, 128 inputs per stage.  Warps 0-7:
-// epilogue (two per TMEM lane quarter, taking turns by 16 tokens).  Then 16
+// epilogue (two per TMEM lane quarter, taking turns by 16 tokens).  Then 12
 // producers: four turn a packed tile into the stage's A tile, 32 rows each, and
-// the groups of four take turns by stage.  Then one warp each for the TMA of
+// the three groups of four take turns by stage.  Then one warp each for the TMA of
 // the packed tiles (8 row tiles in one copy, into a ring), the TMA of the x16
 // tile and the MMAs.  Few row blocks: S CTAs of a cluster share one output
 // tile, each with a part of K, and sum their fp32 tiles through distributed
 // shared memory in rank order.
 //
 // Turns.  A group waits for phases by parity, so it must never be two phases
-// behind: its next stage is `turns` further, the phase it waits for there is
-// the commit of the tile `stages` before that, and it knows (commits are in
-// order) the commit of the tile `stages` before its last one; so turns <=
+// ahead of one: its next stage is kTurns further, the phase it waits for there
+// is the commit of the tile `stages` before that, and it knows (commits are in
+// order) the commit of the tile `stages` before its last one; so kTurns <=
 // stages.  In the packed ring the copy `ring` tiles earlier must be known to
-// have landed: ring >= stages + turns.
+// have landed: ring >= stages + kTurns.
 #include <string.h>
 
 #include <algorithm>
@@ -52,7 +54,7 @@ using namespace op;
 
 constexpr int kRowsA = 128;               // rows of W per tile
 constexpr int kACols = 64;                // TMEM columns of an A stage (128 inputs)
-constexpr int kMaxTile = 192;             // tokens per tile
+constexpr int kMaxTile = 160;             // tokens per tile
 constexpr int kRowTiles = kRowsA / kTileRows;  // 8: producers per stage
 constexpr int kMaxStages = 6;
 constexpr int kBarBytes = 512;
@@ -61,9 +63,9 @@ constexpr int kMaxSmem = 227 * 1024;
 constexpr int kEpiWarps = 8;
 constexpr int kRaw = kRowTiles * kTileBytes;   // packed weights of a stage
 constexpr int kMaxRing = 16;
-constexpr int kProdWarps = 16;
 constexpr int kStageProds = 4;                 // producers of a stage: 32 rows each
-constexpr int kMaxTurns = kProdWarps / kStageProds;
+constexpr int kTurns = 3;                      // groups of them
+constexpr int kProdWarps = kStageProds * kTurns;
 constexpr int kProd0 = kEpiWarps, kRawWarp = kProd0 + kProdWarps, kLoadWarp = kRawWarp + 1, kMmaWarp = kLoadWarp + 1;
 constexpr int kThreads = (kMmaWarp + 1) * 32;
 
@@ -137,7 +139,6 @@ struct GemmParams {
   int split;     // CTAs of a cluster that share a unit (1: units are walked persistently)
   int stages;
   int ring;
-  int turns;     // producer groups in use
   int* err;
   unsigned long long timeout_ns;
 };
@@ -341,13 +342,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A warp turns the 32 rows (two row tiles) of its TMEM lane quarter; four
     // warps make a stage, the sixteen take turns.
     const int q = warp & 3, turn = (warp - kProd0) / kStageProds, g = lane >> 2;
-    // ring slot and stage of every turns-th packed tile, with the parities of
+    // ring slot and stage of every kTurns-th packed tile, with the parities of
     // the phases to wait for
     int slot = turn, st = turn;
     uint32_t rpar = 0, par = 1;
     const unsigned char* mine = raw + 2 * q * kTileBytes;
-    const int n_tiles = turn < p.turns ? total : 0;  // (a group too many has nothing to do)
-    for (int i = turn; i < n_tiles; i += p.turns) {
+    for (int i = turn; i < total; i += kTurns) {
       if (!__all_sync(0xffffffffu, mbar_wait(&raw_full[slot], rpar, p.err, tmo))) break;
       if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], par, p.err, tmo))) break;
       tc_fence_after();
@@ -381,9 +381,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&full[st]);
         mbar_arrive(&raw_empty[slot]);
       }
-      slot += p.turns;
+      slot += kTurns;
       if (slot >= R) slot -= R, rpar ^= 1;
-      st += p.turns;
+      st += kTurns;
       if (st >= S) st -= S, par ^= 1;
     }
   } else if (warp == kRawWarp) {
@@ -530,21 +530,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Shape of a launch.
 struct Plan {
-  int bn, units, split, stages, ring, turns, smem;
+  int bn, units, split, stages, ring, smem;
 };
 
 // slots[i]: clusters of 2^i CTAs that run at once (an SM holds one CTA; GPCs
 // whose SM count is no multiple leave some out: 16 clusters of 8 do not fit).
-// Tokens per tile and CTAs per tile, by an estimate of the time in cycles:
-// a step of 64 inputs takes 2 cycles per token on the tensor core and about
-// 200 in the producers, whichever is longer; 2500 cycles per tile for its
-// start and epilogue, 1500 more for the sum over a cluster.
+// Tokens per tile and CTAs per tile, by an estimate of the time in cycles
+// fitted to measurements: a stage of 128 inputs takes 350 + 3 per token, 500 at
+// least (8192 x 2048-8192: 173 us in tiles of 160 tokens, 183 of 128, 200 of
+// 112, 219 of 96); the epilogue of the last tile 10 per token; the sum over a
+// cluster 2600 + 20 per token (512 x 2048-2048 in tiles of 128: 11.2 us, 11.8
+// shared by two CTAs; 64 x 2048-8192: 9.7 and 9.3).
 Plan plan(int N, int kc, int T, const int (&slots)[4]) {
   Plan best = {};
   double best_t = 0.0;
   const int rb = (N + kRowsA - 1) / kRowsA;
   const int j0 = (T + kMaxTile - 1) / kMaxTile;
-  for (int j = j0; j <= j0 + 8; ++j) {
+  for (int j = j0; j <= j0 + 12; ++j) {
     const int bn = ((T + j - 1) / j + 15) / 16 * 16;
     if (j > j0 && bn < 32) break;
     const int tt = (T + bn - 1) / bn;
@@ -554,8 +556,8 @@ Plan plan(int N, int kc, int T, const int (&slots)[4]) {
       const int split = 1 << i;
       if (i && units > slots[i]) break;
       const int rounds = (units + slots[i] - 1) / slots[i];
-      const double steps = 2.0 * ((kc + split - 1) / split);
-      const double t = rounds * (steps * std::max(2 * bn, 200) + 2500) + (split > 1 ? 1500 : 0);
+      const double t = (double)rounds * ((kc + split - 1) / split) * std::max(350 + 3 * bn, 500) + 10 * bn +
+                       (split > 1 ? 2600 + 20 * bn : 0);
       if (best_t == 0.0 || t < best_t) {
         best_t = t;
         best.bn = bn;
@@ -566,19 +568,18 @@ Plan plan(int N, int kc, int T, const int (&slots)[4]) {
   }
   const int room = kMaxSmem - 1024 - kBarBytes - kXfBytes, stage = best.bn * 256;
   best.stages = std::min(kMaxStages, (512 - 2 * best.bn) / kACols);
-  best.turns = std::min(kMaxTurns, best.stages);
-  best.ring = std::min(kMaxRing, (room - best.stages * stage) / kRaw);  // >= stages + turns, see below
+  best.ring = std::min(kMaxRing, (room - best.stages * stage) / kRaw);  // >= stages + kTurns, see below
   best.smem = best.stages * stage + best.ring * kRaw + kBarBytes + kXfBytes + 1024;
   return best;
 }
 constexpr int ring_at(int bn, int stages) {
   return (kMaxSmem - 1024 - kBarBytes - kXfBytes - stages * bn * 256) / kRaw;
 }
-static_assert(ring_at(192, 2) >= 4 && ring_at(160, 3) >= 6 && ring_at(128, 4) >= 8 && ring_at(96, 5) >= 9 &&
-                  ring_at(64, 6) >= 10 && kMaxRing >= kMaxStages + kMaxTurns,
-              "ring >= stages + turns at the largest tile of every stage count");
-// the stages hold the fp32 tile of a shared unit: stages * 256 bn >= 512 bn
-static_assert((512 - 2 * kMaxTile) / kACols >= 2, "two stages");
+static_assert(ring_at(160, 3) >= 3 + kTurns && ring_at(128, 4) >= 4 + kTurns && ring_at(96, 5) >= 5 + kTurns &&
+                  ring_at(64, 6) >= 6 + kTurns && kMaxRing >= kMaxStages + kTurns,
+              "ring >= stages + kTurns at the largest tile of every stage count");
+static_assert((512 - 2 * kMaxTile) / kACols >= kTurns, "kTurns <= stages");
+// (two or more stages hold the fp32 tile of a shared unit: 256 bn bytes each, 512 bn needed)
 static_assert(8 * (2 * kMaxStages + 2 * kMaxRing + 5) + 4 <= kBarBytes, "barriers");
 
 template <bool kQ8>
@@ -666,7 +667,6 @@ moe_status launch_gemm(moe_linear* L, const XIn& in, int T, uint16_t* y, cudaStr
   p.split = pl.split;
   p.stages = pl.stages;
   p.ring = pl.ring;
-  p.turns = pl.turns;
   p.err = L->err;
   p.timeout_ns = wait_timeout_ns();
   prof::Scope scope("linear_gemm", s);

@@ -63,7 +63,7 @@ struct moe_linear {
   void* x16 = nullptr;      // [max_tokens][K] fp16 operand rows (batches above kExactTokens)
   float* x_f = nullptr;     // [max_tokens] token factors
   CUtensorMap wmap;         // packed tiles, boxes of one tile along K by 8 along N
-  CUtensorMap xmap[12];     // x16 with boxes of 64 inputs by 16 (i + 1) tokens
+  CUtensorMap xmap[10];     // x16 with boxes of 64 inputs by 16 (i + 1) tokens
   int device = 0;
   int num_sms = 0;
   int slots[4] = {};        // clusters of 1, 2, 4, 8 CTAs of the GEMM that run at once
