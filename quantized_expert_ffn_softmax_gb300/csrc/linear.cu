@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(256, kCtas) dot_kernel(const __grid_constant__
     if constexpr (kQ8) {
       uint2 c = make_uint2(0u, 0u);
       if (here) c = *reinterpret_cast<const uint2*>(p.q + (size_t)tok * K + 8 * v);
-      scale = here ? p.qs[(size_t)tok * (K >> 5) + (v >> 2)] : 0.0f;
+      scale = here ? ld_f32(p.qs + (size_t)tok * (K >> 5) + (v >> 2)) : 0.0f;
       hi[0] = __byte_perm(c.x, c.y, 0x5140), hi[1] = __byte_perm(c.x, c.y, 0x7362);
       sum = __dp4a((int)c.x, 0x01010101, __dp4a((int)c.y, 0x01010101, 0));
     } else {
@@ -415,8 +415,8 @@ __global__ void __launch_bounds__(256, kCtas) small_kernel(const __grid_constant
     for (int n = 0; n < NT; ++n) {
       if constexpr (kQ8) {
         v.c[n] = *reinterpret_cast<const uint2*>(p.q + xo[n] + k);
-        v.f[n][0] = p.qs[so[n][0] + (k >> 5)];
-        v.f[n][1] = p.qs[so[n][1] + (k >> 5)];
+        v.f[n][0] = ld_f32(p.qs + so[n][0] + (k >> 5));
+        v.f[n][1] = ld_f32(p.qs + so[n][1] + (k >> 5));
       } else {
         v.c[n] = *reinterpret_cast<const uint4*>(p.x + xo[n] + k);
       }
@@ -674,6 +674,16 @@ moe_status create(const moe_linear_config* c, const moe_linear_weights* w, int o
     return cuda_fail(e, "query the device");
   }
   const int N = c->out_features, K = c->in_features;
+  if (on_device) {  // the pack kernel reads them
+    const Buf src[3] = {{"q", w->q, (size_t)N * (K / 2), 1}, {"s", w->s, (size_t)N * (K / 32) * 2, 2}, {"bias", w->bias, (size_t)N * 4, 4}};
+    for (int i = 0; i < 3; ++i) {
+      moe_status st = (i < 2 || src[i].p) ? check_buf(src[i], L->device) : MOE_OK;
+      if (st != MOE_OK) {
+        delete L;
+        return st;
+      }
+    }
+  }
   L->w.N = N;
   L->w.K = K;
   L->w.kc = (K + kTileK - 1) / kTileK;

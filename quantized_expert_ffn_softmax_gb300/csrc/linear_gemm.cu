@@ -73,8 +73,7 @@ constexpr int kThreads = (kMmaWarp + 1) * 32;
 // Inside every block of 32 inputs, pair i of the 8 inputs 8 t .. 8 t + 7 goes
 // to pair 4 i + t, the order in which A fragments lie in tensor memory.
 template <bool kQ8, int V>
-__global__ void __launch_bounds__(1024) prep_kernel(const XIn in, int K, __half* __restrict__ x16,
-                                                    float* __restrict__ x_f) {
+__global__ void __launch_bounds__(1024) prep_kernel(const XIn in, int K, __half* x16, float* x_f) {
   __shared__ uint32_t red[32];
   dep_wait();
   dep_release();
@@ -89,7 +88,7 @@ __global__ void __launch_bounds__(1024) prep_kernel(const XIn in, int K, __half*
     if (i < nvec) {
       if constexpr (kQ8) {
         const int2 c = *reinterpret_cast<const int2*>(in.q + (size_t)t * K + 8 * i);
-        const float f = in.qs[(size_t)t * (K >> 5) + (i >> 2)];
+        const float f = ld_f32(in.qs + (size_t)t * (K >> 5) + (i >> 2));
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[j][k] = f * (float)(int8_t)((k < 4 ? c.x : c.y) >> (8 * (k & 3)));
       } else {
@@ -287,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // token factors of the tile (the warps agree on going on: the named
       // barrier waits for all of them)
       named_bar_sync(1, kEpiWarps * 32);
-      if (threadIdx.x < bn) xf[threadIdx.x] = (int)threadIdx.x < nt ? p.x_f[t0 + threadIdx.x] : 0.0f;
+      if (threadIdx.x < bn) xf[threadIdx.x] = (int)threadIdx.x < nt ? ld_f32(p.x_f + t0 + threadIdx.x) : 0.0f;
       const bool ok = __all_sync(0xffffffffu, mbar_wait(&tfull[b], (j >> 1) & 1, p.err, tmo));
       if (!named_bar_and(1, kEpiWarps * 32, ok)) break;
       tc_fence_after();
@@ -506,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const uint32_t part = smem_u32(smem) + 16 * lane;
     for (int c = rank + split * warp; c < nt; c += split * (kMmaWarp + 1)) {
-      const float f = p.x_f[t0 + c];
+      const float f = ld_f32(p.x_f + t0 + c);
       float4 v[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = k < split ? ld_cluster_f4(part + c * kRowsA * 4, k) : make_float4(0, 0, 0, 0);
@@ -629,11 +628,6 @@ moe_status gemm_init(moe_linear* L, void* ws) {
     if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   }
   cudaError_t e = cudaFuncSetAttribute(gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-  // the same split between shared memory and L1 as the GEMM's: an SM has to
-  // drain before it can change it
-  for (auto k : {prep_kernel<false, 1>, prep_kernel<false, 4>, prep_kernel<true, 1>, prep_kernel<true, 4>})
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   L->slots[0] = L->num_sms;
   for (int i = 1; i < 4 && e == cudaSuccess; ++i) {
     cudaLaunchConfig_t c = {};

@@ -85,6 +85,15 @@ cudaError_t launch_overlapped(void (*kernel)(KA...), dim3 grid, dim3 block, size
 __device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void dep_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// A float that the kernel before may have written while this one was already
+// resident: never through the read-only path, which takes it to be constant
+// over the kernel's lifetime.
+__device__ __forceinline__ float ld_f32(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+
 // The two bf16 values of a word as floats, and back (round to nearest even).
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }

@@ -159,6 +159,86 @@ def test_refusals(cuda_device):
         lin.forward_q8(q, s[:3])
 
 
+def test_create_refuses_what_the_gpu_cannot_read(cuda_device):
+    N, K = 32, 64
+    q, s, _ = R.quantized(0, N, K)
+    cfg = dict(in_features=K, out_features=N, max_tokens=1)
+    qd, sd = q.to(cuda_device), s.to(cuda_device)
+    odd = torch.zeros(2 * s.numel() + 2, dtype=torch.uint8, device=cuda_device)[1:1 + 2 * s.numel()]
+    for w in (dict(q=q, s=sd), dict(q=qd, s=s), dict(q=qd, s=sd, bias=torch.zeros(N)), dict(q=qd, s=odd)):
+        with pytest.raises(moe.MoeError) as ei:
+            moe.moe_linear_create(cfg, w, True)
+        assert ei.value.status == moe.MOE_ERR_INVALID
+
+
+@pytest.mark.parametrize("T", [1, 3, 8, 12, 40])
+def test_q8_special_values(cuda_device, T):
+    """Zero and NaN scales, the codes' ends; other tokens stay as they are."""
+    N, K = 100, 160
+    lin, w, b = make(N, K, T, True, cuda_device)
+    g = torch.Generator().manual_seed(T)
+    q = torch.randint(-128, 128, (T, K), generator=g).to(torch.int8)
+    q[:, 0], q[:, 1] = -128, 127
+    s = torch.rand(T, K // 32, generator=g) + 0.01
+    s[:, 1] = 0
+    y = lin.forward_q8(q.to(cuda_device), s.to(cuda_device))
+    check(y, R.q8_values(q, s), w, b, bf16=False)
+    s[T - 1, 2] = float("nan")
+    z = lin.forward_q8(q.to(cuda_device), s.to(cuda_device))
+    assert torch.isnan(z[T - 1]).all() and torch.equal(z[:T - 1], y[:T - 1])
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 300, 2048), (2, 300, 2048), (8, 300, 2048), (12, 300, 2048), (40, 300, 2048)])
+@pytest.mark.parametrize("size", [1e-37, 1e-30, 1e30])
+def test_tiny_and_huge_activations(cuda_device, T, N, K, size):
+    lin, w, _ = make(N, K, T, False, cuda_device)
+    x = (acts(T, K).float() * size).bfloat16()
+    y = lin.forward(x.to(cuda_device))
+    # at 1e-37 the result nears fp32's smallest normal number: 2^-126 K absolute
+    y64 = R.product(x.double(), w)
+    bound = R.product_bound(x.double(), w, y64, None, T) + K * 2.0 ** -126
+    assert ((y.double().cpu() - y64).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_captured_after_a_join_of_streams(cuda_device, T):
+    """The input comes from a kernel of another stream, inside one capture."""
+    N, K = 2048, 2048
+    lin, _, _ = make(N, K, T, False, cuda_device)
+    src = acts(T, K).to(cuda_device)
+    x, y, other = torch.zeros_like(src), torch.zeros(T, N, dtype=torch.bfloat16, device=cuda_device), torch.zeros(1 << 22, device=cuda_device)
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            for _ in range(8):
+                other.add_(1)
+            x.copy_(src)
+            x.mul_(2)
+        main.wait_stream(side)
+        moe.moe_linear_forward(lin.handle, x, T, y)
+    want = lin.forward(src * 2)
+    for _ in range(5):
+        x.zero_()
+        y.zero_()
+        g.replay()
+        assert torch.equal(y, want)
+    # the same without a capture
+    for _ in range(5):
+        x.zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(8):
+                other.add_(1)
+            torch.mul(src, 2, out=x)
+        torch.cuda.current_stream().wait_stream(side)
+        moe.moe_linear_forward(lin.handle, x, T, y)
+        assert torch.equal(y, want)
+
+
 @pytest.mark.parametrize("T", [1, 4, 32, 200])
 def test_side_stream_and_graph(cuda_device, T):
     N, K = 1536, 2048

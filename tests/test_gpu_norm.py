@@ -17,7 +17,8 @@ import operators_ref as R
 pytestmark = pytest.mark.gpu
 
 SHAPES = [(1, 32), (1, 2048), (2, 64), (3, 8192), (5, 8224), (7, 2080), (33, 256), (64, 5120), (129, 96), (1, 32768),
-          (2, 16416), (1000, 512), (4097, 128), (700, 2048), (800, 4096), (600, 1056)]
+          (2, 16416), (1000, 512), (4097, 128), (700, 2048), (800, 4096), (600, 1056), (1025, 32),
+          (1100, 288), (1030, 544), (300, 16416), (257, 8224)]
 
 
 def inputs(T, H, residual, gain, seed=0):
