@@ -331,7 +331,9 @@ moe_status moe_linear_forward(moe_linear* linear, const void* x_bf16, int n_toke
 moe_status moe_linear_forward_q8(moe_linear* linear, const int8_t* x_q8, const float* x_scale,
                                  int n_tokens, void* y_bf16, void* stream);
 
-/* moe_status_sync for a projection. */
+/* moe_status_sync for a projection: MOE_ERR_TIMEOUT if a bounded wait of a
+ * kernel ran out (y of that call and of later ones until the word is cleared
+ * is not valid). */
 moe_status moe_linear_status_sync(moe_linear* linear, void* stream);
 
 /* Per-kernel timing of the library's own launches, for measurement (off by

@@ -36,6 +36,7 @@
 // order) the commit of the tile `stages` before its last one; so kTurns <=
 // stages.  In the packed ring the copy `ring` tiles earlier must be known to
 // have landed: ring >= stages + kTurns.
+#include <stdlib.h>
 #include <string.h>
 
 #include <algorithm>
@@ -140,6 +141,9 @@ struct GemmParams {
   int ring;
   int* err;
   unsigned long long timeout_ns;
+  // Test hook: every "full" barrier waits for this many arrivals more than
+  // there are, so the bounded wait runs out and records MOE_ERR_TIMEOUT.
+  int debug_extra_arrivals;
 };
 
 // Word of 8 codes -> 8 weights (code - 8) s' as fp16, in input order; s24, s20
@@ -239,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], kStageProds + 1);  // + the loader's arrive with the tile's bytes
+      mbar_init(&full[s], kStageProds + 1 + p.debug_extra_arrivals);  // + the loader's arrive with the tile's bytes
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < R; ++s) {
@@ -663,6 +667,8 @@ moe_status launch_gemm(moe_linear* L, const XIn& in, int T, uint16_t* y, cudaStr
   p.ring = pl.ring;
   p.err = L->err;
   p.timeout_ns = wait_timeout_ns();
+  const char* dbg = getenv("MOE_DEBUG_UNREACHABLE_BARRIER");
+  p.debug_extra_arrivals = (dbg && atoi(dbg) == 1) ? 1 : 0;
   prof::Scope scope("linear_gemm", s);
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(pl.split > 1 ? pl.units * pl.split : std::min(pl.units, L->num_sms));

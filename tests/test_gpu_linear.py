@@ -239,6 +239,24 @@ def test_captured_after_a_join_of_streams(cuda_device, T):
         assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("T,N,K", [(100, 4111, 2080), (300, 256, 2048), (2000, 3000, 256)])
+def test_bounded_waits_report_a_timeout(cuda_device, monkeypatch, T, N, K):
+    """A barrier that one arrival never reaches: the waits run out, the call
+    reports MOE_ERR_TIMEOUT and the next one is right again."""
+    lin, w, b = make(N, K, T, True, cuda_device)
+    x = acts(T, K)
+    xd = x.to(cuda_device)
+    monkeypatch.setenv("MOE_DEBUG_UNREACHABLE_BARRIER", "1")
+    monkeypatch.setenv("MOE_WAIT_TIMEOUT_US", "20000")
+    lin.forward(xd)
+    assert moe.moe_linear_status_sync(lin.handle) == moe.MOE_ERR_TIMEOUT
+    monkeypatch.delenv("MOE_DEBUG_UNREACHABLE_BARRIER")
+    monkeypatch.delenv("MOE_WAIT_TIMEOUT_US")
+    assert moe.moe_linear_status_sync(lin.handle) == moe.MOE_OK  # cleared
+    check(lin.forward(xd), x.double(), w, b)
+    assert moe.moe_linear_status_sync(lin.handle) == moe.MOE_OK
+
+
 @pytest.mark.parametrize("T", [1, 4, 32, 200])
 def test_side_stream_and_graph(cuda_device, T):
     N, K = 1536, 2048
