@@ -282,11 +282,19 @@ __global__ void __launch_bounds__(256, kCtas) dot_kernel(const __grid_constant__
   __syncthreads();
 
   for (int unit = in.unit0; unit - in.grp < in.units; unit += in.ustep) {  // the same number of turns for every warp
-    float acc[MT][TT][2];
+    float acc[MT][TT][2], rf[MT][2], bias[MT][2];
+    const bool mine = unit < in.units && in.ks == 0 && t == 0;  // the lanes that write
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MT; ++m) {
 #pragma unroll
       for (int k = 0; k < TT; ++k) acc[m][k][0] = acc[m][k][1] = 0.0f;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = (unit * MT + m) * kTileRows + g + 8 * r;
+        rf[m][r] = mine && row < p.w.N ? __ldg(p.w.row_f + row) : 0.0f;
+        bias[m][r] = mine && row < p.w.N && p.w.bias ? __ldg(p.w.bias + row) : 0.0f;
+      }
+    }
     if (unit < in.units) {
       for (int c = in.c0; c < in.c1; ++c) {
         const unsigned char* st = in.next();
@@ -368,18 +376,18 @@ __global__ void __launch_bounds__(256, kCtas) dot_kernel(const __grid_constant__
             }
       }
     }
-    if (unit < in.units && in.ks == 0 && t == 0) {
+    if (mine) {
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int row = (unit * MT + m) * kTileRows + g + 8 * r;
           if (row < p.w.N) {
-            const float rf = __ldg(p.w.row_f + row), bias = p.w.bias ? __ldg(p.w.bias + row) : 0.0f;
 #pragma unroll
             for (int k = 0; k < TT; ++k)
               if (k < p.T)
-                p.y[(size_t)k * p.w.N + row] = __bfloat16_as_ushort(__float2bfloat16_rn(fmaf(acc[m][k][r], rf, bias)));
+                p.y[(size_t)k * p.w.N + row] =
+                    __bfloat16_as_ushort(__float2bfloat16_rn(fmaf(acc[m][k][r], rf[m][r], bias[m][r])));
           }
         }
     }

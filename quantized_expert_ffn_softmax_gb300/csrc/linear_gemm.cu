@@ -64,6 +64,7 @@ constexpr int kMaxSmem = 227 * 1024;
 constexpr int kEpiWarps = 8;
 constexpr int kRaw = kRowTiles * kTileBytes;   // packed weights of a stage
 constexpr int kMaxRing = 16;
+constexpr int kEarly = 2;                      // copies of packed tiles before the kernel before is done
 constexpr int kStageProds = 4;                 // producers of a stage: 32 rows each
 constexpr int kTurns = 3;                      // groups of them
 constexpr int kProdWarps = kStageProds * kTurns;
@@ -76,8 +77,11 @@ constexpr int kThreads = (kMmaWarp + 1) * 32;
 template <bool kQ8, int V>
 __global__ void __launch_bounds__(1024) prep_kernel(const XIn in, int K, __half* x16, float* x_f) {
   __shared__ uint32_t red[32];
-  dep_wait();
+  // The GEMM may start at once: before its own dep_wait it touches nothing but
+  // the weights, and it reads x16 and x_f past L1 (TMA, ld_l2_f32), so that it
+  // cannot meet lines from before this kernel.
   dep_release();
+  dep_wait();
   const int t = blockIdx.x, nvec = K >> 3;
   float v[V][8];
   uint32_t m = 0;
@@ -246,10 +250,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&full[s], kStageProds + 1 + p.debug_extra_arrivals);  // + the loader's arrive with the tile's bytes
       mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < R; ++s) {
-      mbar_init(&raw_full[s], 1);
-      mbar_init(&raw_empty[s], kStageProds);
-    }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], kEpiWarps * 32);
@@ -257,6 +257,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(tdrain, 1);
     fence_mbar_init();
   }
+  const uint64_t tmo = p.timeout_ns;
+  // this CTA's units, and its part of K in packed tiles (128 inputs, a stage)
+  const int split = p.split, rank = split > 1 ? (int)(blockIdx.x % split) : 0;
+  const int u0 = blockIdx.x / split, ustep = split > 1 ? p.units : gridDim.x;
+  const int kc = p.w.kc;
+  const int c0 = rank * kc / split, c1 = (rank + 1) * kc / split;
+  const int total = (p.units - u0 + ustep - 1) / ustep * (c1 - c0);  // stages of this CTA
+
+  // Packed tiles: unit and tile along K of the next copy, its ring slot and
+  // number.  The first copies start before anything else is set up: the
+  // weights are the library's own, there is nothing to wait for.  (Only a few:
+  // a whole ring's copies from every SM delay the operand pass that still runs.)
+  int raw_u = u0, raw_c = c0, raw_slot = 0, raw_i = 0;
+  auto copy_raw = [&]() {
+    if (elect_one()) {
+      mbar_expect_tx(&raw_full[raw_slot], kRaw);
+      tma_load_2d(raw + raw_slot * kRaw, &wmap, raw_c * (kTileBytes / 8), (raw_u % p.n_rb) * kRowTiles,
+                  &raw_full[raw_slot]);
+    }
+    __syncwarp();
+    if (++raw_slot == R) raw_slot = 0;
+    if (++raw_c == c1) raw_c = c0, raw_u += ustep;
+    ++raw_i;
+  };
+  if (warp == kRawWarp) {
+    if (lane == 0) {
+      for (int s = 0; s < R; ++s) {
+        mbar_init(&raw_full[s], 1);
+        mbar_init(&raw_empty[s], kStageProds);
+      }
+      fence_mbar_init();
+    }
+    __syncwarp();
+    while (raw_i < min(kEarly, total)) copy_raw();
+  }
+  if (warp == kLoadWarp && lane == 0)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&xmap)) : "memory");
   if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
@@ -265,14 +302,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint64_t tmo = p.timeout_ns;
-
-  // this CTA's units, and its part of K in packed tiles (128 inputs, a stage)
-  const int split = p.split, rank = split > 1 ? (int)(blockIdx.x % split) : 0;
-  const int u0 = blockIdx.x / split, ustep = split > 1 ? p.units : gridDim.x;
-  const int kc = p.w.kc;
-  const int c0 = rank * kc / split, c1 = (rank + 1) * kc / split;
-  const int total = (p.units - u0 + ustep - 1) / ustep * (c1 - c0);  // stages of this CTA
 
   if (warp < kEpiWarps) {
     // ------------------------------------------------------------ epilogue
@@ -281,24 +310,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     dep_wait();
     dep_release();
     const int r = (warp & 3) * 32 + lane, c_first = 16 * (warp >> 2);
-        const size_t N = p.w.N;
+        const int N = p.w.N;
     int j = 0;
     for (int u = u0; u < p.units; u += ustep, ++j) {
       const int row = (u % p.n_rb) * kRowsA + r, t0 = (u / p.n_rb) * bn;
       const int nt = min(bn, p.T - t0);
       const int b = j & 1;
+      const bool in = row < N;
+      const float rf = in ? __ldg(p.w.row_f + row) * 0x1p24f : 0.0f;  // (loaded while the MMAs run)
+      const float bias = in && p.w.bias ? __ldg(p.w.bias + row) : 0.0f;
       // token factors of the tile (the warps agree on going on: the named
       // barrier waits for all of them)
       named_bar_sync(1, kEpiWarps * 32);
-      if (threadIdx.x < bn) xf[threadIdx.x] = (int)threadIdx.x < nt ? ld_f32(p.x_f + t0 + threadIdx.x) : 0.0f;
+      if (threadIdx.x < bn) xf[threadIdx.x] = (int)threadIdx.x < nt ? ld_l2_f32(p.x_f + t0 + threadIdx.x) : 0.0f;
       const bool ok = __all_sync(0xffffffffu, mbar_wait(&tfull[b], (j >> 1) & 1, p.err, tmo));
       if (!named_bar_and(1, kEpiWarps * 32, ok)) break;
       tc_fence_after();
       const uint32_t tb = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(b * bn);
       if (split == 1) {
-        const bool in = row < p.w.N;
-        const float rf = in ? __ldg(p.w.row_f + row) * 0x1p24f : 0.0f;
-        const float bias = in && p.w.bias ? __ldg(p.w.bias + row) : 0.0f;
         for (int c = c_first; c < nt; c += 16 * (kEpiWarps / 4)) {
           uint32_t v[16];
           tmem_ld16(tb + c, v);
@@ -391,30 +420,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kRawWarp) {
     // ------------------------------------------------------------ packed tiles
-    // The weights are the library's own: the first copies wait for nothing.
-    int slot = 0, i = 0;
-    uint32_t par = 1;
-    for (int u = u0; u < p.units && i >= 0; u += ustep) {
-      for (int c = c0; c < c1; ++c, ++i) {
-        if (i == R) {
-          dep_wait();
-          dep_release();
-        }
-        if (!__all_sync(0xffffffffu, mbar_wait(&raw_empty[slot], par, p.err, tmo))) {
-          i = -1 << 30;
-          break;
-        }
-        if (elect_one()) {
-          mbar_expect_tx(&raw_full[slot], kRaw);
-          tma_load_2d(raw + slot * kRaw, &wmap, c * (kTileBytes / 8), (u % p.n_rb) * kRowTiles, &raw_full[slot]);
-        }
-        __syncwarp();
-        if (++slot == R) slot = 0, par ^= 1;
-      }
-    }
-    if (i >= 0 && i <= R) {
-      dep_wait();
-      dep_release();
+    dep_wait();
+    dep_release();
+    while (raw_i < min(R, total)) copy_raw();
+    uint32_t par = 0;  // of the slot's next "empty" phase (copy R waits for the first)
+    while (raw_i < total) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&raw_empty[raw_slot], par, p.err, tmo))) break;
+      copy_raw();
+      if (raw_slot == 0) par ^= 1;
     }
     settle(p.err);
   } else if (warp == kLoadWarp) {
@@ -496,7 +509,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (split > 1) {
-    cluster_publish(warp);  // every partial tile is in its CTA's shared memory
     // this CTA sums the tokens congruent to its rank, four rows per thread
     const int t0 = (u0 / p.n_rb) * bn, nt = min(bn, p.T - t0);
     const int row = (u0 % p.n_rb) * kRowsA + 4 * lane;
@@ -507,9 +519,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       rf[i] = in ? __ldg(p.w.row_f + row + i) * 0x1p24f : 0.0f;
       bias[i] = in && p.w.bias ? __ldg(p.w.bias + row + i) : 0.0f;
     }
+    cluster_publish(warp);  // every partial tile is in its CTA's shared memory
     const uint32_t part = smem_u32(smem) + 16 * lane;
     for (int c = rank + split * warp; c < nt; c += split * (kMmaWarp + 1)) {
-      const float f = ld_f32(p.x_f + t0 + c);
+      const float f = xf[c];
       float4 v[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = k < split ? ld_cluster_f4(part + c * kRowsA * 4, k) : make_float4(0, 0, 0, 0);

@@ -79,9 +79,10 @@ cudaError_t launch_overlapped(void (*kernel)(KA...), dim3 grid, dim3 block, size
 
 // Every thread of an overlapped kernel calls dep_wait() before its first
 // access to memory that another kernel may have written or may still read,
-// and only then lets the next kernel in with dep_release(): a kernel that is
-// let in therefore starts after everything before the current one is done,
-// so no line of a reused buffer can sit in an L1 from an older reader.
+// and, but for kernels that say why not, only then lets the next kernel in with
+// dep_release(): a kernel that is let in therefore starts after everything
+// before the current one is done, so no line of a reused buffer can sit in an
+// L1 from an older reader.
 __device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void dep_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -91,6 +92,13 @@ __device__ __forceinline__ void dep_release() { asm volatile("griddepcontrol.lau
 __device__ __forceinline__ float ld_f32(const float* p) {
   float v;
   asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+
+// The same, past L1.
+__device__ __forceinline__ float ld_l2_f32(const float* p) {
+  float v;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p));
   return v;
 }
 
