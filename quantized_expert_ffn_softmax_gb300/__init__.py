@@ -132,12 +132,16 @@ def lib():
 def _ptr(a) -> Optional[int]:
     if a is None:
         return None
-    if isinstance(a, int):
-        return a
-    if hasattr(a, "data_ptr"):
+    try:  # a tensor, first: every argument of a decode-sized call counts
+        p = a.data_ptr()
+    except AttributeError:
+        pass
+    else:
         if not a.is_contiguous():
             raise ValueError("tensor must be contiguous")
-        return a.data_ptr()
+        return p
+    if isinstance(a, int):
+        return a
     if hasattr(a, "ctypes"):
         if not a.flags["C_CONTIGUOUS"]:
             raise ValueError("array must be C-contiguous")
@@ -171,7 +175,7 @@ def _current_stream() -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        return _current_stream()
+        return _current() if _current is not None else _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
