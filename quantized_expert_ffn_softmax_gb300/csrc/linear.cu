@@ -743,17 +743,17 @@ moe_status create(const moe_linear_config* c, const moe_linear_weights* w, int o
   return MOE_OK;
 }
 
-// 9 to 16 tokens: the mma.sync kernel starts about 4 us sooner than the GEMM
-// with its operand pass, but takes 0.21 us per million weights against 0.12
-// (measured at 16 tokens: 9.1 against 10.3 us at 4096 x 8192, 58 against 38 us
-// at 2048 x 131073).
-bool use_gemm(const moe_linear* L, int T) {
-  return T > kSmallTokens || (T > kExactTokens && (long long)L->w.N * L->w.K > 48000000ll);
+// 9 to 16 tokens: the mma.sync kernel starts a few us sooner than the GEMM with
+// its operand pass, but takes longer per weight, most of all when 8-bit x has to
+// be converted again for every tile (16 tokens: 8.7 against 7.5 us at 2048 x
+// 10240, 17.9 against 14.9 at 5120 x 10240, in 8 bits 26 against 15).
+bool use_gemm(const moe_linear* L, const XIn& in, int T) {
+  return T > kSmallTokens || (T > kExactTokens && (long long)L->w.N * L->w.K > (in.x ? 16000000ll : 8000000ll));
 }
 
 moe_status run(moe_linear* L, const XIn& in, int T, void* y, void* stream) {
   cudaStream_t s = (cudaStream_t)stream;
-  if (use_gemm(L, T)) return launch_gemm(L, in, T, static_cast<uint16_t*>(y), s);
+  if (use_gemm(L, in, T)) return launch_gemm(L, in, T, static_cast<uint16_t*>(y), s);
   SmallParams p = {};
   p.w = L->w;
   p.T = T;

@@ -21,7 +21,9 @@
 // 192 tokens, the stages wait for their copies: 8192 x 2048-8192 takes 198 us
 // against 173).
 //
-// One CTA per SM, warp-specialised, 128 inputs per stage.  Warps 0-7:
+// One CTA per SM, warp-specialised, 128 inputs per stage (KS = 1), or 256 for
+// tiles of up to 64 tokens (KS = 2), whose MMAs are so short that the waits
+// between two stages count.  Warps 0-7:
 // epilogue (two per TMEM lane quarter, taking turns by 16 tokens).  Then 12
 // producers: four turn a packed tile into the stage's A tile, 32 rows each, and
 // the three groups of four take turns by stage.  Then one warp each for the TMA of
@@ -54,7 +56,8 @@ using namespace dev;
 using namespace op;
 
 constexpr int kRowsA = 128;               // rows of W per tile
-constexpr int kACols = 64;                // TMEM columns of an A stage (128 inputs)
+constexpr int kACols = 64;                // TMEM columns of 128 inputs of an A stage
+constexpr int kWideTile = 64;             // largest tile with 256 inputs per stage
 constexpr int kMaxTile = 160;             // tokens per tile
 constexpr int kRowTiles = kRowsA / kTileRows;  // 8: producers per stage
 constexpr int kMaxStages = 6;
@@ -224,6 +227,8 @@ __device__ __forceinline__ void tmem_st_16x128b_x16(uint32_t taddr, const uint32
       : "memory");
 }
 
+// KS: packed tiles (of 128 inputs) per stage.
+template <int KS>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ GemmParams p, const __grid_constant__ CUtensorMap xmap,
                 const __grid_constant__ CUtensorMap wmap) {
@@ -231,10 +236,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                          ~static_cast<uintptr_t>(1023));
   const int bn = p.bn, S = p.stages;
-  const int half_b = bn * 128, stage_bytes = 2 * half_b;  // the x16 tile
+  const int half_b = bn * 128, stage_bytes = 2 * KS * half_b;  // the x16 tile
   const int R = p.ring;
-  unsigned char* raw = smem + S * stage_bytes;  // R packed tiles of 128 rows x 128 inputs
-  float* xf = reinterpret_cast<float*>(raw + R * kRaw);  // [kMaxTile] token factors
+  unsigned char* raw = smem + S * stage_bytes;  // R times the packed weights of a stage
+  float* xf = reinterpret_cast<float*>(raw + R * KS * kRaw);  // [kMaxTile] token factors
   uint64_t* full = reinterpret_cast<uint64_t*>(xf + kMaxTile);
   uint64_t* empty = full + kMaxStages;
   uint64_t* raw_full = empty + kMaxStages;
@@ -258,10 +263,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   const uint64_t tmo = p.timeout_ns;
-  // this CTA's units, and its part of K in packed tiles (128 inputs, a stage)
+  // this CTA's units, and its part of K in stages
   const int split = p.split, rank = split > 1 ? (int)(blockIdx.x % split) : 0;
   const int u0 = blockIdx.x / split, ustep = split > 1 ? p.units : gridDim.x;
-  const int kc = p.w.kc;
+  const int kc = (p.w.kc + KS - 1) / KS;  // (a last half stage reads zeros)
   const int c0 = rank * kc / split, c1 = (rank + 1) * kc / split;
   const int total = (p.units - u0 + ustep - 1) / ustep * (c1 - c0);  // stages of this CTA
 
@@ -272,9 +277,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   int raw_u = u0, raw_c = c0, raw_slot = 0, raw_i = 0;
   auto copy_raw = [&]() {
     if (elect_one()) {
-      mbar_expect_tx(&raw_full[raw_slot], kRaw);
-      tma_load_2d(raw + raw_slot * kRaw, &wmap, raw_c * (kTileBytes / 8), (raw_u % p.n_rb) * kRowTiles,
-                  &raw_full[raw_slot]);
+      mbar_expect_tx(&raw_full[raw_slot], KS * kRaw);
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+        tma_load_2d(raw + (raw_slot * KS + k) * kRaw, &wmap, (raw_c * KS + k) * (kTileBytes / 8),
+                    (raw_u % p.n_rb) * kRowTiles, &raw_full[raw_slot]);
     }
     __syncwarp();
     if (++raw_slot == R) raw_slot = 0;
@@ -384,8 +391,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], par, p.err, tmo))) break;
       tc_fence_after();
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {  // row tile 2 q + h
-        const unsigned char* tl = mine + slot * kRaw + h * kTileBytes;
+      for (int kh = 0; kh < 2 * KS; ++kh) {  // packed tile kh / 2, row tile 2 q + h
+        const int h = kh & 1;
+        const unsigned char* tl = mine + (slot * KS + (kh >> 1)) * kRaw + h * kTileBytes;
         const uint4 w0 = *reinterpret_cast<const uint4*>(tl + 16 * lane);
         const uint4 w1 = *reinterpret_cast<const uint4*>(tl + 512 + 16 * lane);
         const uint4 sc = *reinterpret_cast<const uint4*>(tl + kTileCodes + 16 * g);
@@ -403,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         put(0, w0.y, w0.w, sc.z, 1);
         put(2, w1.x, w1.z, sc.y, 0);
         put(2, w1.y, w1.w, sc.w, 1);
-        tmem_st_16x128b_x16(tmem + ((uint32_t)(32 * q + 16 * h) << 16) + (uint32_t)(2 * bn + kACols * st), o);
+        tmem_st_16x128b_x16(tmem + ((uint32_t)(32 * q + 16 * h) << 16) + (uint32_t)(2 * bn + kACols * (st * KS + (kh >> 1))), o);
       }
       fence_proxy_async_smem();  // the ring slot's reads come before the next copy into it
       tmem_wait_st();
@@ -446,9 +454,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (elect_one()) {
           unsigned char* B = smem + st * stage_bytes;
-          mbar_expect_tx(&full[st], (uint32_t)(2 * half_b));
-          tma_load_2d(B, &xmap, c * kTileK, t0, &full[st]);
-          tma_load_2d(B + half_b, &xmap, c * kTileK + 64, t0, &full[st]);  // past K: zeros
+          mbar_expect_tx(&full[st], (uint32_t)stage_bytes);
+#pragma unroll
+          for (int k = 0; k < 2 * KS; ++k)  // (past K: zeros)
+            tma_load_2d(B + k * half_b, &xmap, c * KS * kTileK + 64 * k, t0, &full[st]);
         }
         __syncwarp();
         if (++st == S) st = 0, par ^= 1;
@@ -481,12 +490,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t a = tmem + (uint32_t)(2 * bn + kACols * st);  // 16 inputs: 8 columns
-          umma_f16_ts(d, a, db, idesc, acc);
+          const uint32_t a = tmem + (uint32_t)(2 * bn + kACols * KS * st);  // 16 inputs: 8 columns
 #pragma unroll
-          for (int k = 1; k < 4; ++k) umma_f16_ts(d, a + 8 * k, db + 2 * k, idesc, 1u);
+          for (int h = 0; h < 2 * KS; ++h)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) umma_f16_ts(d, a + 32 + 8 * k, db + half + 2 * k, idesc, 1u);
+            for (int k = 0; k < 4; ++k)
+              umma_f16_ts(d, a + 32 * h + 8 * k, db + h * half + 2 * k, idesc, h + k == 0 ? acc : 1u);
           umma_commit(&empty[st]);
         }
         __syncwarp();
@@ -544,9 +553,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+constexpr int kRoom = kMaxSmem - 1024 - kBarBytes - kXfBytes;  // for stages and ring
+
 // Shape of a launch.
 struct Plan {
-  int bn, units, split, stages, ring, smem;
+  int bn, units, split, wide, stages, ring, smem;
 };
 
 // slots[i]: clusters of 2^i CTAs that run at once (an SM holds one CTA; GPCs
@@ -568,11 +579,12 @@ Plan plan(int N, int kc, int T, const int (&slots)[4]) {
     const int tt = (T + bn - 1) / bn;
     if ((long long)rb * tt > 0x3fffffff) break;
     const int units = rb * tt;
-    for (int i = 0; i < 4 && (1 << i) <= kc; ++i) {
+    const int ks = bn <= kWideTile ? 2 : 1, n_stages = (kc + ks - 1) / ks;
+    for (int i = 0; i < 4 && (1 << i) <= n_stages; ++i) {
       const int split = 1 << i;
       if (i && units > slots[i]) break;
       const int rounds = (units + slots[i] - 1) / slots[i];
-      const double t = (double)rounds * ((kc + split - 1) / split) * std::max(350 + 3 * bn, 500) + 10 * bn +
+      const double t = (double)rounds * ((n_stages + split - 1) / split) * (ks == 2 ? 900 : std::max(350 + 3 * bn, 500)) + 10 * bn +
                        (split > 1 ? 2600 + 20 * bn : 0);
       if (best_t == 0.0 || t < best_t) {
         best_t = t;
@@ -582,18 +594,20 @@ Plan plan(int N, int kc, int T, const int (&slots)[4]) {
       }
     }
   }
-  const int room = kMaxSmem - 1024 - kBarBytes - kXfBytes, stage = best.bn * 256;
-  best.stages = std::min(kMaxStages, (512 - 2 * best.bn) / kACols);
-  best.ring = std::min(kMaxRing, (room - best.stages * stage) / kRaw);  // >= stages + kTurns, see below
-  best.smem = best.stages * stage + best.ring * kRaw + kBarBytes + kXfBytes + 1024;
+  best.wide = best.bn <= kWideTile;
+  const int ks = best.wide ? 2 : 1, stage = best.bn * 256 * ks, raw = kRaw * ks;
+  best.stages = std::min(kMaxStages, (512 - 2 * best.bn) / (kACols * ks));
+  best.ring = std::min(kMaxRing, (kRoom - best.stages * stage) / raw);  // >= stages + kTurns, see below
+  best.smem = best.stages * stage + best.ring * raw + kBarBytes + kXfBytes + 1024;
   return best;
 }
-constexpr int ring_at(int bn, int stages) {
-  return (kMaxSmem - 1024 - kBarBytes - kXfBytes - stages * bn * 256) / kRaw;
+constexpr bool ring_ok(int bn, int stages, int ks) {
+  return (kRoom - stages * bn * 256 * ks) / (kRaw * ks) >= stages + kTurns;
 }
-static_assert(ring_at(160, 3) >= 3 + kTurns && ring_at(128, 4) >= 4 + kTurns && ring_at(96, 5) >= 5 + kTurns &&
-                  ring_at(64, 6) >= 6 + kTurns && kMaxRing >= kMaxStages + kTurns,
+static_assert(ring_ok(160, 3, 1) && ring_ok(128, 4, 1) && ring_ok(96, 5, 1) && ring_ok(64, 3, 2) &&
+                  kMaxRing >= kMaxStages + kTurns,
               "ring >= stages + kTurns at the largest tile of every stage count");
+static_assert((512 - 2 * kWideTile) / (2 * kACols) >= kTurns, "kTurns <= stages");
 static_assert((512 - 2 * kMaxTile) / kACols >= kTurns, "kTurns <= stages");
 // (two or more stages hold the fp32 tile of a shared unit: 256 bn bytes each, 512 bn needed)
 static_assert(8 * (2 * kMaxStages + 2 * kMaxRing + 5) + 4 <= kBarBytes, "barriers");
@@ -644,7 +658,9 @@ moe_status gemm_init(moe_linear* L, void* ws) {
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   }
-  cudaError_t e = cudaFuncSetAttribute(gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  cudaError_t e = cudaFuncSetAttribute(gemm_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(gemm_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   L->slots[0] = L->num_sms;
   for (int i = 1; i < 4 && e == cudaSuccess; ++i) {
     cudaLaunchConfig_t c = {};
@@ -657,7 +673,7 @@ moe_status gemm_init(moe_linear* L, void* ws) {
     c.dynamicSmemBytes = kMaxSmem;
     c.attrs = at;
     c.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&L->slots[i], gemm_kernel, &c);
+    e = cudaOccupancyMaxActiveClusters(&L->slots[i], gemm_kernel<1>, &c);
   }
   if (e != cudaSuccess) return cuda_fail(e, "gemm configuration");
   return MOE_OK;
@@ -696,7 +712,7 @@ moe_status launch_gemm(moe_linear* L, const XIn& in, int T, uint16_t* y, cudaStr
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   c.attrs = at;
   c.numAttrs = 2;
-  e = cudaLaunchKernelEx(&c, gemm_kernel, p, L->xmap[pl.bn / 16 - 1],
+  e = cudaLaunchKernelEx(&c, pl.wide ? gemm_kernel<2> : gemm_kernel<1>, p, L->xmap[pl.bn / 16 - 1],
                          L->wmap);
   if (e != cudaSuccess) return cuda_fail(e, "linear gemm launch");
   return MOE_OK;
