@@ -320,8 +320,8 @@ void moe_linear_destroy(moe_linear* linear);
  * inputs (off by at most 2^-14 of the block's largest |x|, exact down to 1/64
  * of it), and above 8 tokens x and W may be rounded to fp16 operands, each
  * token and each row of W scaled by a power of two.  A token with an infinity
- * or NaN in x has unspecified non-finite values in y; other tokens are not
- * affected. */
+ * or NaN in x, or with |x| above 2^100, may have any non-finite values in y;
+ * other tokens are not affected. */
 moe_status moe_linear_forward(moe_linear* linear, const void* x_bf16, int n_tokens, void* y_bf16,
                               void* stream);
 

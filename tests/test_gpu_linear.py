@@ -42,7 +42,7 @@ def test_small_batches(cuda_device, T, N, K, bias):
     assert moe.moe_linear_status_sync(lin.handle) == moe.MOE_OK
 
 
-@pytest.mark.parametrize("T,N,K", SMALL + [(33, 100, 64), (100, 4111, 2080), (300, 777, 1056), (40, 70, 16416)])
+@pytest.mark.parametrize("T,N,K", SMALL + [(9, 4000, 2080), (16, 5000, 2048), (33, 100, 64), (100, 4111, 2080), (300, 777, 1056), (40, 70, 16416)])
 def test_q8(cuda_device, T, N, K):
     lin, w, b = make(N, K, T, True, cuda_device)
     g = torch.Generator().manual_seed(T + N + K)
