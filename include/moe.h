@@ -288,8 +288,8 @@ moe_status moe_add_rmsnorm_q8(const void* x_bf16, const void* residual_bf16, con
 typedef struct moe_linear moe_linear; /* opaque, owned by the library */
 
 /* Limits: 32 <= in_features <= 32768, a multiple of 32; 1 <= out_features <=
- * 1048576; 1 <= max_tokens <= 65536 (above 8 the handle also holds a
- * workspace of about 2 * max_tokens * in_features bytes). */
+ * 1048576; 1 <= max_tokens <= 65536 (unless all calls are small, the handle also
+ * holds a workspace of about 2 * max_tokens * in_features bytes). */
 typedef struct {
   int32_t in_features;  /* K */
   int32_t out_features; /* N */
@@ -315,10 +315,10 @@ void moe_linear_destroy(moe_linear* linear);
 
 /* y = x W^T + bias: x bf16 [n_tokens][K], y bf16 [n_tokens][N], results
  * bit-identical from call to call.  Calls on one handle must not overlap on
- * the GPU (they share its workspace).  Sums are fp32, the weights exact up to
- * 8 tokens; one or two bf16 tokens may be taken as integers per block of 32
- * inputs (off by at most 2^-14 of the block's largest |x|, exact down to 1/64
- * of it), and above 8 tokens x and W may be rounded to fp16 operands, each
+ * the GPU (they share its workspace).  Sums are fp32.  One token: W is exact,
+ * x may be taken as integers per block of 32 inputs (off by at most 2^-14 of
+ * the block's largest |x|, exact down to 1/64 of it).  2 to 8 tokens with K * N
+ * at most 2^25: x and W are exact.  Otherwise both may be rounded to fp16, each
  * token and each row of W scaled by a power of two.  A token with an infinity
  * or NaN in x, or with |x| above 2^100, may have any non-finite values in y;
  * other tokens are not affected. */

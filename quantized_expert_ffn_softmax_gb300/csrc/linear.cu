@@ -5,8 +5,8 @@
 // straight from HBM through a ring in shared memory into registers; what
 // bounds these kernels is the number of instructions per weight, first of all
 // the unpacking on the integer pipe.
-//   dot_kernel    1 or 2 tokens in bf16, up to 4 in 8 bits: integer dot
-//                 products (dp4a) of the codes with x as integers
+//   dot_kernel    1 token in bf16, up to 2 in 8 bits: integer dot products
+//                 (dp4a) of the codes with x as integers
 //   small_kernel  up to 16 tokens: the legacy tensor path (mma.sync), W the
 //                 16-row operand A unpacked exactly to bf16 integers, up to two
 //                 8-token column tiles operand B
@@ -561,6 +561,7 @@ int warps_per_unit(int units, int kc, int slots) {
 }
 
 constexpr int kDotSmem = 64 * 1024;  // largest x area of dot_kernel
+constexpr int kDotDeep = 36 * 1024;  // largest with eight stages (two CTAs in 227 KB)
 
 template <int MT, int ST, int kCtas>
 struct Variant {
@@ -569,12 +570,13 @@ struct Variant {
   int part;     // bytes of the partial sums when warps share a unit
 };
 
-// A kernel variant: one tile per unit and eight stages at two CTAs per SM for
-// the dot products (28.3 us at 2048 x 131073; two tiles: 29.9, six stages at
-// three CTAs: 30.1).  `call` is what to do with it.
-template <int TT, bool kQ8, typename F>
+// A kernel variant; `call` is what to do with it.  Dot products: one tile per
+// unit at two CTAs per SM, with eight stages while both fit beside x (26 us at
+// 1 x 2048-131073; measured before other steps: two tiles 29.9 us, six stages at
+// three CTAs 30.1, this 28.3), else with four.
+template <int TT, int ST, bool kQ8, typename F>
 cudaError_t with_dot(F&& call) {
-  constexpr int MT = 1, ST = 8, kCtas = 2;
+  constexpr int MT = 1, kCtas = 2;
   return call(Variant<MT, ST, kCtas>{dot_kernel<TT, MT, ST, kCtas, kQ8>, kDotSmem, 8 * MT * TT * 64});
 }
 template <int NT, int MT, int ST, bool kQ8, typename F>
@@ -592,11 +594,12 @@ struct SetSmem {
 };
 // The shared-memory limits of every variant, on the current device.
 cudaError_t small_init() {
-  cudaError_t e = with_dot<1, false>(SetSmem());
-  if (e == cudaSuccess) e = with_dot<2, false>(SetSmem());
-  if (e == cudaSuccess) e = with_dot<1, true>(SetSmem());
-  if (e == cudaSuccess) e = with_dot<2, true>(SetSmem());
-  if (e == cudaSuccess) e = with_dot<4, true>(SetSmem());
+  cudaError_t e = with_dot<1, 8, false>(SetSmem());
+  if (e == cudaSuccess) e = with_dot<1, 4, false>(SetSmem());
+  if (e == cudaSuccess) e = with_dot<1, 8, true>(SetSmem());
+  if (e == cudaSuccess) e = with_dot<1, 4, true>(SetSmem());
+  if (e == cudaSuccess) e = with_dot<2, 8, true>(SetSmem());
+  if (e == cudaSuccess) e = with_dot<2, 4, true>(SetSmem());
   if (e == cudaSuccess) e = with_small<1, 1, 8, false>(SetSmem());
   if (e == cudaSuccess) e = with_small<1, 2, 4, false>(SetSmem());
   if (e == cudaSuccess) e = with_small<2, 2, 4, false>(SetSmem());
@@ -622,13 +625,16 @@ struct Launch {
 
 template <bool kQ8>
 cudaError_t launch_small(const SmallParams& p, int num_sms, cudaStream_t s) {
-  const int tt = p.T <= 2 ? p.T : 4, x_bytes = tt * p.w.kc * (kTileK / 8) * (kQ8 ? 16 : 24);
-  if (p.T <= (kQ8 ? 4 : 2) && x_bytes <= kDotSmem) {
+  // (2 tokens in bf16, 4 in 8 bits: the MMA kernel is as fast or faster, 2.6 to
+  // 3.1 us at 2048 x 2048, 11.4 to 19.2 at 8192 x 8192)
+  const int x_bytes = p.T * p.w.kc * (kTileK / 8) * (kQ8 ? 16 : 24);
+  if (p.T <= (kQ8 ? kDotTokensQ8 : 1) && x_bytes <= kDotSmem) {
     prof::Scope scope(kQ8 ? "linear_dot_q8" : "linear_dot", s);
     const Launch go{p, x_bytes, num_sms, s};
-    if (tt == 1) return with_dot<1, kQ8>(go);
-    if (tt == 2) return with_dot<2, kQ8>(go);
-    if constexpr (kQ8) return with_dot<4, true>(go);
+    const bool deep = x_bytes <= kDotDeep;
+    if constexpr (kQ8)
+      if (p.T == 2) return deep ? with_dot<2, 8, true>(go) : with_dot<2, 4, true>(go);
+    return deep ? with_dot<1, 8, kQ8>(go) : with_dot<1, 4, kQ8>(go);
   }
   prof::Scope scope(kQ8 ? "linear_small_q8" : "linear_small", s);
   const Launch go{p, 0, num_sms, s};
@@ -706,7 +712,7 @@ moe_status create(const moe_linear_config* c, const moe_linear_weights* w, int o
     moe_linear_destroy(L);
     return cuda_fail(err, what);
   };
-  if ((e = cudaMalloc(&L->block, o_ws + gemm_workspace(K, c->max_tokens))) != cudaSuccess) return bad(e, "cudaMalloc(linear weights)");
+  if ((e = cudaMalloc(&L->block, o_ws + gemm_workspace(N, K, c->max_tokens))) != cudaSuccess) return bad(e, "cudaMalloc(linear weights)");
   char* base = static_cast<char*>(L->block);
   L->w.tiles = reinterpret_cast<const uint8_t*>(base);
   L->w.row_f = reinterpret_cast<const float*>(base + o_rf);
@@ -743,12 +749,18 @@ moe_status create(const moe_linear_config* c, const moe_linear_weights* w, int o
   return MOE_OK;
 }
 
-// 9 to 16 tokens: the mma.sync kernel starts a few us sooner than the GEMM with
-// its operand pass, but takes longer per weight, most of all when 8-bit x has to
-// be converted again for every tile (16 tokens: 8.7 against 7.5 us at 2048 x
-// 10240, 17.9 against 14.9 at 5120 x 10240, in 8 bits 26 against 15).
+// Up to 16 tokens the mma.sync kernel starts a few us sooner than the GEMM with
+// its operand pass but takes longer per weight, most of all above 8 tokens (two
+// MMAs per weight fragment) and in 8 bits (x is converted again for every tile).
+// Measured, mma.sync against GEMM, us: 8 tokens 8192 x 8192 11.6 / 13.0, 2048 x
+// 65536 25.5 / 19.9; 8 bits 4096 x 8192 8.2 / 8.2, 8192 x 8192 14.4 / 13.1; 16
+// tokens 2048 x 10240 8.7 / 6.6, 5120 x 10240 17.9 / 11.6.
 bool use_gemm(const moe_linear* L, const XIn& in, int T) {
-  return T > kSmallTokens || (T > kExactTokens && (long long)L->w.N * L->w.K > (in.x ? 16000000ll : 8000000ll));
+  const long long weights = (long long)L->w.N * L->w.K;
+  if (T > kSmallTokens) return true;
+  if (T > 8) return weights > (in.x ? 16000000ll : kGemmWeights9);
+  if (T > (in.x ? 1 : kDotTokensQ8)) return weights > (in.x ? 80000000ll : kGemmWeights2);
+  return false;
 }
 
 moe_status run(moe_linear* L, const XIn& in, int T, void* y, void* stream) {

@@ -632,14 +632,14 @@ cudaError_t launch_prep(moe_linear* L, const XIn& in, int T, cudaStream_t s) {
 
 }  // namespace
 
-size_t gemm_workspace(int K, int max_tokens) {
-  if (max_tokens <= kExactTokens) return 0;
+size_t gemm_workspace(int N, int K, int max_tokens) {
+  if (!needs_gemm(N, K, max_tokens)) return 0;
   return (((size_t)max_tokens * K * 2 + 255) & ~(size_t)255) + (size_t)max_tokens * 4;
 }
 
 moe_status gemm_init(moe_linear* L, void* ws) {
   const int T = L->cfg.max_tokens, K = L->w.K;
-  if (T <= kExactTokens) return MOE_OK;
+  if (!needs_gemm(L->w.N, K, T)) return MOE_OK;
   L->x16 = ws;
   L->x_f = reinterpret_cast<float*>(static_cast<char*>(ws) + (((size_t)T * K * 2 + 255) & ~(size_t)255));
   PFN_cuTensorMapEncodeTiled_v12000 enc = tmap_encode_fn();

@@ -28,8 +28,10 @@ constexpr int kTileRows = 16;
 constexpr int kTileK = 128;
 constexpr int kTileCodes = 1024;
 constexpr int kTileBytes = 1152;
-constexpr int kExactTokens = 8;   // largest batch that never takes the GEMM
+constexpr int kDotTokensQ8 = 2;   // largest 8-bit batch of the dot-product kernel
 constexpr int kSmallTokens = 16;  // largest batch of the small-batch kernels
+// fewest weights (N x K) that take the GEMM with 9 to 16 and with 2 to 8 tokens
+constexpr long long kGemmWeights9 = 8000000, kGemmWeights2 = 1 << 25;
 
 struct Weights {
   const uint8_t* tiles;
@@ -40,7 +42,7 @@ struct Weights {
   int nt;             // tiles along N
 };
 
-// linear_gemm.cu: batches above kExactTokens.
+// linear_gemm.cu: batches of the GEMM.
 // x as fp16, every token scaled by a power of two to a largest magnitude in
 // [1, 2): rows of x16 and the inverse factors.
 struct XIn {
@@ -48,7 +50,12 @@ struct XIn {
   const int8_t* q;    // [T][K] codes and
   const float* qs;    // [T][K/32] scales
 };
-size_t gemm_workspace(int K, int max_tokens);
+// Whether any call of a handle takes the GEMM.
+inline bool needs_gemm(int N, int K, int max_tokens) {
+  const long long w = (long long)N * K;
+  return max_tokens > kSmallTokens || (max_tokens > 8 && w > kGemmWeights9) || (max_tokens > 1 && w > kGemmWeights2);
+}
+size_t gemm_workspace(int N, int K, int max_tokens);
 moe_status gemm_init(moe_linear* L, void* ws);
 moe_status launch_gemm(moe_linear* L, const XIn& in, int T, uint16_t* y, cudaStream_t s);
 

@@ -19,8 +19,7 @@ def product(x64, w64, bias=None):
     return y if bias is None else y + bias.double()
 
 
-EXACT_TOKENS = 8  # largest batch whose weights are never rounded
-DOT_TOKENS = 2    # largest batch whose bf16 x may be taken as integers per block of 32
+EXACT_TOKENS, EXACT_WEIGHTS = 8, 1 << 25  # the largest call whose operands are not rounded to fp16
 
 
 def product_bound(x64, w64, y64, bias=None, tokens=1, bf16=True):
@@ -31,9 +30,9 @@ def product_bound(x64, w64, y64, bias=None, tokens=1, bf16=True):
     magnitudes (the tensor cores truncate: twice fp32's step 2^-23), a few more
     for the scales: (32 + K/32 + 8) 2^-22 of sum |x||w|.  (One long chain on the
     tensor cores adds 16 products at a time, K/16 additions: K/16 2^-22.)
-    Up to DOT_TOKENS bf16 tokens: x as multiples of 2^(e - 13), with 2^e at most
+    One bf16 token: x as multiples of 2^(e - 13), with 2^e at most
     the largest |x| of the block: off by 2^-14 of that at most.
-    Above EXACT_TOKENS the operands may be fp16: each weight is rounded once,
+    Above EXACT_TOKENS or EXACT_WEIGHTS the operands may be fp16: each weight is rounded once,
     2^-11 of itself, or, below 2^-14 in units where the row's largest scale is
     at least 2^-9, twice by 2^-25, so 2^-15 of the row's largest scale, which is
     at most its largest |weight| where that block has a code other than 8.
@@ -43,10 +42,10 @@ def product_bound(x64, w64, y64, bias=None, tokens=1, bf16=True):
     ax, aw = x64.abs(), w64.abs()
     mag = ax @ aw.T + (0 if bias is None else bias.double().abs())
     err = mag * ((32 + K / 16 + 8) * 2.0 ** -22)
-    if bf16 and tokens <= DOT_TOKENS:
+    if bf16 and tokens == 1:
         top = ax.view(-1, K // 32, 32).amax(-1).repeat_interleave(32, 1)
         err = err + 2.0 ** -14 * (top @ aw.T)
-    if tokens > EXACT_TOKENS:
+    if tokens > EXACT_TOKENS or (tokens > 1 and w64.numel() > EXACT_WEIGHTS):
         err = err + 2.0 ** -11 * mag + 2.0 ** -15 * ax.sum(1, keepdim=True) * aw.amax(1)
         err = err + 2.0 ** -25 * ax.amax(1, keepdim=True) * aw.sum(1)
     return err + (y64.abs() + err) * 2.0 ** -8 + 1e-38

@@ -27,7 +27,7 @@ def check(y, x64, w64, bias, tokens=None, bf16=True):
     assert (off <= bound).all(), (off / bound).max().item()
 
 
-SMALL = [(1, 16, 32), (2, 16, 32), (4, 30, 32), (1, 50, 16384), (1, 30, 32768), (2, 3000, 10272), (3, 700, 2048), (1, 1, 32), (1, 17, 64), (1, 2048, 2048), (2, 100, 96), (3, 2049, 160), (4, 33, 8192), (5, 640, 1056),
+SMALL = [(1, 16, 32), (2, 16, 32), (4, 30, 32), (1, 50, 16384), (1, 30, 32768), (2, 3000, 10272), (2, 90000, 512), (5, 45000, 2048), (1, 40, 12288), (3, 700, 2048), (1, 1, 32), (1, 17, 64), (1, 2048, 2048), (2, 100, 96), (3, 2049, 160), (4, 33, 8192), (5, 640, 1056),
          (8, 257, 2080), (9, 1000, 256), (16, 4099, 512), (17, 48, 2048), (31, 515, 1024), (32, 1024, 4096),
          (1, 40000, 256), (8, 5000, 4128), (32, 16, 32768), (24, 9000, 128)]
 
@@ -42,7 +42,7 @@ def test_small_batches(cuda_device, T, N, K, bias):
     assert moe.moe_linear_status_sync(lin.handle) == moe.MOE_OK
 
 
-@pytest.mark.parametrize("T,N,K", SMALL + [(9, 4000, 2080), (16, 5000, 2048), (33, 100, 64), (100, 4111, 2080), (300, 777, 1056), (40, 70, 16416)])
+@pytest.mark.parametrize("T,N,K", SMALL + [(9, 4000, 2080), (16, 5000, 2048), (3, 18000, 2048), (2, 18000, 2048), (2, 60, 16384), (33, 100, 64), (100, 4111, 2080), (300, 777, 1056), (40, 70, 16416)])
 def test_q8(cuda_device, T, N, K):
     lin, w, b = make(N, K, T, True, cuda_device)
     g = torch.Generator().manual_seed(T + N + K)
