@@ -22,9 +22,8 @@ namespace {
 // Scratch of the allocation-free entry point: 128 KiB per GPU that loads the
 // library, held until the process exits.  Every call uses it.  Carve:
 // grid-barrier counter | error word | router logits [4][E] | shared-gate
-// logits [4] | two fp32 layer-output accumulators [2][4][H].  The largest
-// shape that fits has H = 2048 with any E, or H = 3072 with E <= 1024;
-// H = 4096 needs 129 KiB and more and is refused.
+// logits [4] | two fp32 layer-output accumulators [2][4][H].  H = 2048
+// fits with any E; H = 4096 needs 129 KiB and more and is refused.
 constexpr size_t kNoAllocScratchBytes = 128u << 10;
 __device__ __align__(256) unsigned char g_noalloc_scratch[kNoAllocScratchBytes];
 
