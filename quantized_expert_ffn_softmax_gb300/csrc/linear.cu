@@ -13,6 +13,7 @@
 // In both the result of every 32-input block is multiplied by its scale in
 // fp32.  Larger batches: linear_gemm.cu.
 #include <math.h>
+#include <stdlib.h>
 
 #include <new>
 #include <type_traits>
@@ -677,6 +678,8 @@ moe_status create(const moe_linear_config* c, const moe_linear_weights* w, int o
   if (c->max_tokens < 1 || c->max_tokens > 65536)
     return fail(MOE_ERR_INVALID, "max_tokens=%d outside [1, 65536]", c->max_tokens);
   if (!w || !w->q || !w->s) return fail(MOE_ERR_INVALID, "a required weight pointer is NULL");
+  const char* fault = getenv("MOE_FAULT_ALLOC");
+  if (fault && atoi(fault) == 1) return fail(MOE_ERR_OOM, "allocation failure injected by MOE_FAULT_ALLOC");
   moe_linear* L = new (std::nothrow) moe_linear();
   if (!L) return fail(MOE_ERR_OOM, "out of host memory");
   L->cfg = *c;

@@ -129,6 +129,89 @@ def test_extreme_scales(cuda_device, T):
     check(lin.forward(x.to(cuda_device)), x.double(), w, None)
 
 
+@pytest.mark.parametrize("T", [1, 3, 12, 100])
+def test_bad_rows_of_weights_stay_apart(cuda_device, T):
+    """Negative, infinite and NaN scales: only their own rows feel them."""
+    N, K = 200, 288
+    q, s, w = R.quantized(11, N, K)
+    sign = 1 - 2 * torch.randint(0, 2, s.shape, generator=torch.Generator().manual_seed(3)).half()
+    s = s * sign
+    w = w * sign.double().repeat_interleave(32, 1)
+    x = acts(T, K)
+    lin = moe.MoELinear(dict(in_features=K, out_features=N, max_tokens=T), dict(q=q, s=s), False)
+    y = lin.forward(x.to(cuda_device))
+    check(y, x.double(), w, None)
+    s[17, 3], s[150, 0] = float("inf"), float("nan")
+    lin = moe.MoELinear(dict(in_features=K, out_features=N, max_tokens=T), dict(q=q, s=s), False)
+    z = lin.forward(x.to(cuda_device))
+    good = [n for n in range(N) if n not in (17, 150)]
+    assert torch.equal(z[:, good], y[:, good])
+    assert torch.isnan(z[:, 150]).all() and not torch.isfinite(z[:, 17]).any()
+
+
+def test_output_past_32_bits(cuda_device):
+    """An output of 5.2 GB: the last rows against a call on those tokens alone."""
+    T, N, K = 65536, 40003, 64
+    lin, w, b = make(N, K, T, True, cuda_device)
+    x = torch.randn(T, K, device=cuda_device).bfloat16()
+    y = lin.forward(x)
+    assert y.numel() * 2 > 1 << 32
+    for t in (0, 32768, T - 40):
+        assert torch.equal(y[t:t + 40], lin.forward(x[t:t + 40].contiguous()))
+    check(y[T - 3:], x[T - 3:].cpu().double(), w, b, T)
+    assert moe.moe_linear_status_sync(lin.handle) == moe.MOE_OK
+
+
+@pytest.mark.parametrize("T", [1, 5, 40])
+def test_weights_past_32_bits(cuda_device, T):
+    """5.5 GB of packed weights: the last rows against the definition."""
+    N, K = 600001, 16384
+    g = torch.Generator(device=cuda_device).manual_seed(1)
+    q = torch.randint(0, 256, (N, K // 2), generator=g, device=cuda_device, dtype=torch.uint8)
+    s = (torch.rand(N, K // 32, generator=g, device=cuda_device) * 0.02).half()
+    lin = moe.MoELinear(dict(in_features=K, out_features=N, max_tokens=T), dict(q=q, s=s), True)
+    qt, st = q[-50:].cpu(), s[-50:].cpu()
+    del q, s
+    torch.cuda.empty_cache()
+    x = acts(T, K)
+    y = lin.forward(x.to(cuda_device))[:, -50:]
+    c = torch.stack((qt & 15, qt >> 4), -1).view(50, K // 32, 32).double() - 8
+    w = (c * st.double()[..., None]).view(50, K)
+    check(y, x.double(), w, None, max(T, 9) if T > 1 else 1)
+
+
+@pytest.mark.parametrize("Ta,Tb", [(100, 300), (1, 64), (8, 700)])
+def test_two_handles_on_two_streams(cuda_device, Ta, Tb):
+    a, _, _ = make(1500, 2048, Ta, True, cuda_device)
+    b, _, _ = make(2048, 1056, Tb, False, cuda_device, seed=4)
+    xa, xb = acts(Ta, 2048).to(cuda_device), acts(Tb, 1056).to(cuda_device)
+    ya, yb = a.forward(xa), b.forward(xb)
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    za, zb = (torch.zeros((20,) + tuple(y.shape), dtype=y.dtype, device=cuda_device) for y in (ya, yb))
+    torch.cuda.synchronize()
+    for i in range(20):
+        moe.moe_linear_forward(a.handle, xa, Ta, za[i], sa)
+        moe.moe_linear_forward(b.handle, xb, Tb, zb[i], sb)
+    torch.cuda.synchronize()
+    assert all(torch.equal(z, ya) for z in za) and all(torch.equal(z, yb) for z in zb)
+    assert moe.moe_linear_status_sync(a.handle) == moe.MOE_OK == moe.moe_linear_status_sync(b.handle)
+
+
+def test_profile_names_the_kernels(cuda_device):
+    lin, _, _ = make(512, 512, 64, False, cuda_device)
+    moe.moe_profile_read()
+    moe.moe_profile_enable(True)
+    try:
+        for T in (1, 8, 64):
+            lin.forward(acts(T, 512).to(cuda_device))
+        moe.add_rmsnorm(acts(3, 512).to(cuda_device))
+    finally:
+        moe.moe_profile_enable(False)
+    got = moe.moe_profile_read()
+    assert {k: v[0] for k, v in got.items()} == {"linear_dot": 1, "linear_small": 1, "linear_prep": 1, "linear_gemm": 1,
+                                                 "add_rmsnorm": 1}
+
+
 def test_refusals(cuda_device):
     N, K, T = 64, 128, 40
     lin, _, _ = make(N, K, T, False, cuda_device)

@@ -119,6 +119,26 @@ def test_guard_rows_stay(cuda_device):
     assert (q[T] == 9).all() and (s[T] == 7).all()
 
 
+def test_offsets_past_32_bits(cuda_device):
+    """Rows of a 4.3 GB input against calls on those rows alone."""
+    T, H = 65536, 32768
+    x = torch.randn(1024, H, device=cuda_device).bfloat16().repeat(T // 1024, 1)
+    x[T - 1] = 3
+    h, u = torch.empty_like(x), torch.empty_like(x)
+    moe.moe_add_rmsnorm(x, x, None, 1e-6, T, H, h, u)
+    for t in (0, 40000, T - 1):
+        row = x[t:t + 1].contiguous()
+        h1, u1 = moe.add_rmsnorm(row, row)
+        assert torch.equal(h[t], h1[0]) and torch.equal(u[t], u1[0])
+    del h, u
+    q = torch.empty(T, H, dtype=torch.int8, device=cuda_device)
+    s = torch.empty(T, H // 32, device=cuda_device)
+    moe.moe_add_rmsnorm_q8(x, None, None, 1e-6, T, H, None, q, s)
+    for t in (0, 40000, T - 1):
+        _, q1, s1 = moe.add_rmsnorm(x[t:t + 1].contiguous(), q8=True)
+        assert torch.equal(q[t], q1[0]) and torch.equal(s[t], s1[0])
+
+
 def test_refusals(cuda_device):
     T, H = 4, 64
     x, r, w = (dev(t, cuda_device) for t in inputs(T, H, True, True))

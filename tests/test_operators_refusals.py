@@ -37,6 +37,15 @@ def test_linear_create_rejects_missing_weights(lib, missing):
     assert "NULL" in moe.moe_last_error()
 
 
+def test_linear_create_reports_a_failed_allocation(lib, monkeypatch):
+    monkeypatch.setenv("MOE_FAULT_ALLOC", "1")
+    out = ctypes.c_void_p(1)
+    cfg = moe.moe_linear_config(64, 8, 1)
+    w = moe.moe_linear_weights(16, 16, None)
+    assert lib.moe_linear_create(ctypes.byref(cfg), ctypes.byref(w), 0, ctypes.byref(out)) == moe.MOE_ERR_OOM
+    assert out.value is None
+
+
 def test_calls_reject_null_handles(lib):
     assert lib.moe_linear_create(None, None, 0, None) == moe.MOE_ERR_INVALID
     out = ctypes.c_void_p(1)
