@@ -219,6 +219,13 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t saddr, int rank) {
   return v;
 }
 
+// mbar_wait of a whole warp: the same answer on every lane.  The test by itself
+// first: the code around a wait that succeeds at once is what costs.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* err, uint64_t timeout_ns) {
+  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, timeout_ns));
+}
+
 // On an error path a stage may stay incomplete: gives the copies already
 // issued time to land before the CTA can exit.
 __device__ __forceinline__ void settle(int* err) {
@@ -346,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // barrier waits for all of them)
       named_bar_sync(1, kEpiWarps * 32);
       if (threadIdx.x < bn) xf[threadIdx.x] = (int)threadIdx.x < nt ? ld_l2_f32(p.x_f + t0 + threadIdx.x) : 0.0f;
-      const bool ok = __all_sync(0xffffffffu, mbar_wait(&tfull[b], (j >> 1) & 1, p.err, tmo));
+      const bool ok = warp_wait(&tfull[b], (j >> 1) & 1, p.err, tmo);
       if (!named_bar_and(1, kEpiWarps * 32, ok)) break;
       tc_fence_after();
       const uint32_t tb = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(b * bn);
@@ -403,8 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t rpar = 0, par = 1;
     const unsigned char* mine = raw + 2 * q * kTileBytes;
     for (int i = turn; i < total; i += kTurns) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&raw_full[slot], rpar, p.err, tmo))) break;
-      if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], par, p.err, tmo))) break;
+      if (!warp_wait(&raw_full[slot], rpar, p.err, tmo)) break;
+      if (!warp_wait(&empty[st], par, p.err, tmo)) break;
       tc_fence_after();
 #pragma unroll
       for (int kh = 0; kh < 2 * KS; ++kh) {  // packed tile kh / 2, row tile 2 q + h
@@ -449,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (raw_i < min(R, total)) copy_raw();
     uint32_t par = 0;  // of the slot's next "empty" phase (copy R waits for the first)
     while (raw_i < total) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&raw_empty[raw_slot], par, p.err, tmo))) break;
+      if (!warp_wait(&raw_empty[raw_slot], par, p.err, tmo)) break;
       copy_raw();
       if (raw_slot == 0) par ^= 1;
     }
@@ -464,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int u = u0; u < p.units && alive; u += ustep) {
       const int t0 = (u / p.n_rb) * bn;
       for (int c = c0; c < c1; ++c) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], par, p.err, tmo))) {
+        if (!warp_wait(&empty[st], par, p.err, tmo)) {
           alive = false;
           break;
         }
@@ -494,13 +501,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t par = 0;
     for (int u = u0; u < p.units; u += ustep, ++j) {
       const int b = j & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(&tempty[b], ((j >> 1) & 1) ^ 1, p.err, tmo))) break;
+      if (!warp_wait(&tempty[b], ((j >> 1) & 1) ^ 1, p.err, tmo)) break;
       tc_fence_after();
       const uint32_t d = tmem + (uint32_t)(b * bn);
       bool ok = true;
       uint32_t acc = 0;
       for (int c = c0; c < c1; ++c) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&full[st], par, p.err, tmo))) {
+        if (!warp_wait(&full[st], par, p.err, tmo)) {
           ok = false;
           break;
         }
@@ -514,7 +521,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               umma_f16_ts(d, a + 32 * h + 8 * k, db + h * half + 2 * k, idesc, h + k == 0 ? acc : 1u);
           umma_commit(&empty[st]);
         }
-        __syncwarp();
         acc = 1;
         db += dstep;
         if (++st == S) st = 0, par ^= 1, db = d0;
