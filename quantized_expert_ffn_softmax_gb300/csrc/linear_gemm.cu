@@ -399,16 +399,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < kRawWarp) {
     // ------------------------------------------------------------ producers
-    dep_wait();
-    dep_release();
     // A warp turns the 32 rows (two row tiles) of its TMEM lane quarter; four
-    // warps make a stage, the sixteen take turns.
+    // warps make a stage, the three groups take turns.  Weights and tensor memory
+    // are all they touch, so with 256 inputs per stage a first stage whose copy
+    // is one of the early ones comes before the kernel before is done (64 x
+    // 4096-4096: 8.9 -> 8.4 us; nothing gained with 128).  Later stages wait for
+    // others' progress, which must not run into the time limit while the kernel
+    // before runs.
     const int q = warp & 3, turn = (warp - kProd0) / kStageProds, g = lane >> 2;
     // ring slot and stage of every kTurns-th packed tile, with the parities of
     // the phases to wait for
     int slot = turn, st = turn;
     uint32_t rpar = 0, par = 1;
     const unsigned char* mine = raw + 2 * q * kTileBytes;
+    if (KS == 1 || turn >= kEarly) dep_wait();
     for (int i = turn; i < total; i += kTurns) {
       if (!warp_wait(&raw_full[slot], rpar, p.err, tmo)) break;
       if (!warp_wait(&empty[st], par, p.err, tmo)) break;
@@ -444,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&full[st]);
         mbar_arrive(&raw_empty[slot]);
       }
+      if (KS > 1 && i == turn) dep_wait();
       slot += kTurns;
       if (slot >= R) slot -= R, rpar ^= 1;
       st += kTurns;
