@@ -19,7 +19,8 @@
 // move 192 bytes a cycle of its 128.  Two accumulators and the A stages share
 // the 512 columns: 4 stages at 128 tokens a tile, 3 at 160, the most (with 2, at
 // 192 tokens, the stages wait for their copies: 8192 x 2048-8192 takes 198 us
-// against 173).
+// against 173).  Where no CTA has a second tile there is one accumulator, and
+// tiles go up to 224 tokens (700 x 8192-2048: 26.5 -> 24.5 us).
 //
 // One CTA per SM, warp-specialised, 128 inputs per stage (KS = 1), or 256 for
 // tiles of up to 64 tokens (KS = 2), whose MMAs are so short that what lies
@@ -34,7 +35,7 @@
 //
 // Measured (GPU time, operand pass included): 8192 x 2048-8192 170 us, 1.6
 // PFLOP/s, bound by the MMAs and what the power limit leaves of their clock;
-// 32 x 2048-131073 31 us, 5.2 TB/s, bound by HBM; 32 x 4096-8192 9.1 us, of
+// 32 x 2048-131073 31 us, 5.2 TB/s, bound by HBM; 32 x 4096-8192 8.4 us, of
 // which about 5 are the operand pass, the first copies' latency and the sum over
 // the cluster.
 //
@@ -64,11 +65,11 @@ using namespace op;
 constexpr int kRowsA = 128;               // rows of W per tile
 constexpr int kACols = 64;                // TMEM columns of 128 inputs of an A stage
 constexpr int kWideTile = 64;             // largest tile with 256 inputs per stage
-constexpr int kMaxTile = 160;             // tokens per tile
+constexpr int kMaxTile = 160;             // tokens per tile with two accumulators
 constexpr int kRowTiles = kRowsA / kTileRows;  // 8
 constexpr int kMaxStages = 6;
 constexpr int kBarBytes = 512;
-constexpr int kXfBytes = kMaxTile * 4;
+constexpr int kXfBytes = kMaxOneTile * 4;
 constexpr int kMaxSmem = 227 * 1024;
 constexpr int kEpiWarps = 8;
 constexpr int kRaw = kRowTiles * kTileBytes;   // packed weights of a stage
@@ -156,7 +157,8 @@ struct GemmParams {
   const float* x_f;
   uint16_t* y;
   int T;
-  int bn;        // tokens per tile: a multiple of 16, 16 .. kMaxTile
+  int bn;        // tokens per tile: a multiple of 16, 16 .. kMaxOneTile
+  int a_col;     // first TMEM column of the A stages
   int n_rb;      // row blocks
   int units;     // row blocks x token tiles
   int split;     // CTAs of a cluster that share a unit (1: units are walked persistently)
@@ -262,8 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int half_b = bn * 128, stage_bytes = 2 * KS * half_b;  // the x16 tile
   const int R = p.ring;
   unsigned char* raw = smem + S * stage_bytes;  // R times the packed weights of a stage
-  float* xf = reinterpret_cast<float*>(raw + R * KS * kRaw);  // [kMaxTile] token factors
-  uint64_t* full = reinterpret_cast<uint64_t*>(xf + kMaxTile);
+  float* xf = reinterpret_cast<float*>(raw + R * KS * kRaw);  // [kMaxOneTile] token factors
+  uint64_t* full = reinterpret_cast<uint64_t*>(xf + kMaxOneTile);
   uint64_t* empty = full + kMaxStages;
   uint64_t* raw_full = empty + kMaxStages;
   uint64_t* raw_empty = raw_full + kMaxRing;
@@ -438,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         put(0, w0.y, w0.w, sc.z, 1);
         put(2, w1.x, w1.z, sc.y, 0);
         put(2, w1.y, w1.w, sc.w, 1);
-        tmem_st_16x128b_x16(tmem + ((uint32_t)(32 * q + 16 * h) << 16) + (uint32_t)(2 * bn + kACols * (st * KS + (kh >> 1))), o);
+        tmem_st_16x128b_x16(tmem + ((uint32_t)(32 * q + 16 * h) << 16) + (uint32_t)(p.a_col + kACols * (st * KS + (kh >> 1))), o);
       }
       fence_proxy_async_smem();  // the ring slot's reads come before the next copy into it
       tmem_wait_st();
@@ -518,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t a = tmem + (uint32_t)(2 * bn + kACols * KS * st);  // 16 inputs: 8 columns
+          const uint32_t a = tmem + (uint32_t)(p.a_col + kACols * KS * st);  // 16 inputs: 8 columns
 #pragma unroll
           for (int h = 0; h < 2 * KS; ++h)
 #pragma unroll
@@ -582,9 +584,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 constexpr int kRoom = kMaxSmem - 1024 - kBarBytes - kXfBytes;  // for stages and ring
 
+// Stages and rings of a launch: tokens per tile, packed tiles per stage, and
+// accumulators (one if no CTA has a second tile).
+struct Rings {
+  int a_col, stages, ring, smem;
+};
+constexpr Rings rings(int bn, int ks, int accs) {
+  const int stage = bn * 256 * ks, raw = kRaw * ks, a_col = (accs * bn + 31) / 32 * 32;
+  const int fit = std::min((512 - a_col) / (kACols * ks), (kRoom - kTurns * raw) / (stage + raw));
+  const int stages = std::min(kMaxStages, fit), ring = std::min(kMaxRing, (kRoom - stages * stage) / raw);
+  return {a_col, stages, ring, stages * stage + ring * raw + kBarBytes + kXfBytes + 1024};
+}
+constexpr bool rings_ok() {
+  for (int accs = 1; accs <= 2; ++accs)
+    for (int ks = 1; ks <= 2; ++ks)
+      for (int bn = 16; bn <= (ks == 2 ? kWideTile : accs == 2 ? kMaxTile : kMaxOneTile); bn += 16) {
+        const Rings r = rings(bn, ks, accs);
+        if (r.stages < kTurns || r.ring < r.stages + kTurns || r.a_col < accs * bn ||
+            r.a_col + r.stages * ks * kACols > 512 || r.smem > kMaxSmem)
+          return false;
+        if (r.stages * bn * 256 * ks < bn * kRowsA * 4) return false;  // the stages hold the fp32 tile of a shared unit
+      }
+  return true;
+}
+static_assert(rings_ok(), "kTurns <= stages, ring >= stages + kTurns, and all fits");
+static_assert(8 * (2 * kMaxStages + 2 * kMaxRing + 5) + 4 <= kBarBytes, "barriers");
+
 // Shape of a launch.
 struct Plan {
-  int bn, units, split, wide, stages, ring, smem;
+  int bn, units, split, wide;
+  Rings r;
 };
 
 // slots[i]: clusters of 2^i CTAs that run at once (an SM holds one CTA; GPCs
@@ -599,8 +628,8 @@ Plan plan(int N, int kc, int T, const int (&slots)[4]) {
   Plan best = {};
   double best_t = 0.0;
   const int rb = (N + kRowsA - 1) / kRowsA;
-  const int j0 = (T + kMaxTile - 1) / kMaxTile;
-  for (int j = j0; j <= j0 + 12; ++j) {
+  const int j0 = (T + kMaxOneTile - 1) / kMaxOneTile, j1 = (T + kMaxTile - 1) / kMaxTile + 12;
+  for (int j = j0; j <= j1; ++j) {
     const int bn = ((T + j - 1) / j + 15) / 16 * 16;
     if (j > j0 && bn < 32) break;
     const int tt = (T + bn - 1) / bn;
@@ -611,6 +640,7 @@ Plan plan(int N, int kc, int T, const int (&slots)[4]) {
       const int split = 1 << i;
       if (i && units > slots[i]) break;
       const int rounds = (units + slots[i] - 1) / slots[i];
+      if (bn > kMaxTile && rounds > 1) continue;
       const double t = (double)rounds * ((n_stages + split - 1) / split) * (ks == 2 ? 900 : std::max(350 + 3 * bn, 500)) + 10 * bn +
                        (split > 1 ? 2600 + 20 * bn : 0);
       if (best_t == 0.0 || t < best_t) {
@@ -622,22 +652,9 @@ Plan plan(int N, int kc, int T, const int (&slots)[4]) {
     }
   }
   best.wide = best.bn <= kWideTile;
-  const int ks = best.wide ? 2 : 1, stage = best.bn * 256 * ks, raw = kRaw * ks;
-  best.stages = std::min(kMaxStages, (512 - 2 * best.bn) / (kACols * ks));
-  best.ring = std::min(kMaxRing, (kRoom - best.stages * stage) / raw);  // >= stages + kTurns, see below
-  best.smem = best.stages * stage + best.ring * raw + kBarBytes + kXfBytes + 1024;
+  best.r = rings(best.bn, best.wide ? 2 : 1, best.split > 1 || best.units <= slots[0] ? 1 : 2);
   return best;
 }
-constexpr bool ring_ok(int bn, int stages, int ks) {
-  return (kRoom - stages * bn * 256 * ks) / (kRaw * ks) >= stages + kTurns;
-}
-static_assert(ring_ok(160, 3, 1) && ring_ok(128, 4, 1) && ring_ok(96, 5, 1) && ring_ok(64, 3, 2) &&
-                  kMaxRing >= kMaxStages + kTurns,
-              "ring >= stages + kTurns at the largest tile of every stage count");
-static_assert((512 - 2 * kWideTile) / (2 * kACols) >= kTurns, "kTurns <= stages");
-static_assert((512 - 2 * kMaxTile) / kACols >= kTurns, "kTurns <= stages");
-// (two or more stages hold the fp32 tile of a shared unit: 256 bn bytes each, 512 bn needed)
-static_assert(8 * (2 * kMaxStages + 2 * kMaxRing + 5) + 4 <= kBarBytes, "barriers");
 
 template <bool kQ8>
 cudaError_t launch_prep(moe_linear* L, const XIn& in, int T, cudaStream_t s) {
@@ -669,7 +686,7 @@ moe_status gemm_init(moe_linear* L, void* ws) {
   L->x_f = reinterpret_cast<float*>(static_cast<char*>(ws) + (((size_t)T * K * 2 + 255) & ~(size_t)255));
   PFN_cuTensorMapEncodeTiled_v12000 enc = tmap_encode_fn();
   if (!enc) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-  for (int i = 0; i < kMaxTile / 16; ++i) {
+  for (int i = 0; i < kMaxOneTile / 16; ++i) {
     cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)T};
     cuuint64_t strides[1] = {(cuuint64_t)K * 2};
     cuuint32_t box[2] = {64, (cuuint32_t)(16 * (i + 1))};
@@ -723,8 +740,9 @@ moe_status launch_gemm(moe_linear* L, const XIn& in, int T, uint16_t* y, cudaStr
   p.n_rb = (L->w.N + kRowsA - 1) / kRowsA;
   p.units = pl.units;
   p.split = pl.split;
-  p.stages = pl.stages;
-  p.ring = pl.ring;
+  p.a_col = pl.r.a_col;
+  p.stages = pl.r.stages;
+  p.ring = pl.r.ring;
   p.err = L->err;
   p.timeout_ns = wait_timeout_ns();
   const char* dbg = getenv("MOE_DEBUG_UNREACHABLE_BARRIER");
@@ -733,7 +751,7 @@ moe_status launch_gemm(moe_linear* L, const XIn& in, int T, uint16_t* y, cudaStr
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(pl.split > 1 ? pl.units * pl.split : std::min(pl.units, L->num_sms));
   c.blockDim = dim3(kThreads);
-  c.dynamicSmemBytes = pl.smem;
+  c.dynamicSmemBytes = pl.r.smem;
   c.stream = s;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

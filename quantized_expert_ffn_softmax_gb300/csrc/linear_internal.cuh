@@ -33,6 +33,9 @@ constexpr int kSmallTokens = 16;  // largest batch of the small-batch kernels
 // fewest weights (N x K) that take the GEMM with 9 to 16 and with 2 to 8 tokens
 constexpr long long kGemmWeights9 = 8000000, kGemmWeights2 = 1 << 25;
 
+// Largest token tile of the GEMM (no CTA has a second one).
+constexpr int kMaxOneTile = 224;
+
 struct Weights {
   const uint8_t* tiles;
   const float* row_f;  // [N] scale = stored scale * row_f
@@ -67,10 +70,10 @@ struct moe_linear {
   moe::lin::Weights w;
   void* block = nullptr;
   int* err = nullptr;
-  void* x16 = nullptr;      // [max_tokens][K] fp16 operand rows (batches above kExactTokens)
+  void* x16 = nullptr;      // [max_tokens][K] fp16 operand rows (batches of the GEMM)
   float* x_f = nullptr;     // [max_tokens] token factors
   CUtensorMap wmap;         // packed tiles, boxes of one tile along K by 8 along N
-  CUtensorMap xmap[10];     // x16 with boxes of 64 inputs by 16 (i + 1) tokens
+  CUtensorMap xmap[moe::lin::kMaxOneTile / 16];    // x16 with boxes of 64 inputs by 16 (i + 1) tokens
   int device = 0;
   int num_sms = 0;
   int slots[4] = {};        // clusters of 1, 2, 4, 8 CTAs of the GEMM that run at once

@@ -67,6 +67,19 @@ def test_large_batches(cuda_device, T, N, K, bias):
     assert moe.moe_linear_status_sync(lin.handle) == moe.MOE_OK
 
 
+# one tile per SM and few row blocks: tiles of more than 160 tokens, whole and
+# shared by the CTAs of a cluster, with rows and tokens left over
+@pytest.mark.parametrize("T,N,K", [(322, 7700, 352), (161, 1600, 6752), (700, 2044, 8192), (213, 1500, 6784)])
+def test_large_tiles(cuda_device, T, N, K):
+    lin, w, b = make(N, K, T, True, cuda_device)
+    x = acts(T, K)
+    y = torch.full(((T + 1) * N,), 7.0, dtype=torch.bfloat16, device=cuda_device)
+    moe.moe_linear_forward(lin.handle, x.to(cuda_device), T, y[:T * N])
+    check(y[:T * N].view(T, N), x.double(), w, b)
+    assert (y[T * N:] == 7.0).all()
+    assert moe.moe_linear_status_sync(lin.handle) == moe.MOE_OK
+
+
 @pytest.mark.parametrize("T", [1, 5, 32, 33, 300])
 def test_device_and_host_weights_agree(cuda_device, T):
     N, K = 1030, 608
