@@ -33,11 +33,11 @@
 // share one output tile, each with a part of K, and sum their fp32 tiles through
 // distributed shared memory in rank order.
 //
-// Measured (GPU time, operand pass included): 8192 x 2048-8192 170 us, 1.6
-// PFLOP/s, bound by the MMAs and what the power limit leaves of their clock;
-// 32 x 2048-131073 31 us, 5.2 TB/s, bound by HBM; 32 x 4096-8192 8.4 us, of
-// which about 5 are the operand pass, the first copies' latency and the sum over
-// the cluster.
+// Measured (GPU time, operand pass included): 8192 x 2048-8192 167 us, 1.6
+// PFLOP/s (189 over seconds), bound by the MMAs and what the power limit leaves
+// of their clock; 1024 x 2048-5120 19.1 us, 1.1 PFLOP/s; 32 x 2048-131073 31
+// us, 5.2 TB/s, bound by HBM; 32 x 4096-8192 8.4 us, of which about 5 are the
+// operand pass, the first copies' latency and the sum over the cluster.
 //
 // Turns.  A group waits for phases by parity, so it must never be two phases
 // ahead of one: its next stage is kTurns further, the phase it waits for there
