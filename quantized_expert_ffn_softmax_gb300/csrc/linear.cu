@@ -754,15 +754,19 @@ moe_status create(const moe_linear_config* c, const moe_linear_weights* w, int o
 
 // Up to 16 tokens the mma.sync kernel starts a few us sooner than the GEMM with
 // its operand pass but takes longer per weight, most of all above 8 tokens (two
-// MMAs per weight fragment) and in 8 bits (x is converted again for every tile).
-// Measured, mma.sync against GEMM, us: 8 tokens 8192 x 8192 11.6 / 13.0, 2048 x
-// 65536 25.5 / 19.9; 8 bits 4096 x 8192 8.2 / 8.2, 8192 x 8192 14.4 / 13.1; 16
-// tokens 2048 x 10240 8.7 / 6.6, 5120 x 10240 17.9 / 11.6.
+// MMAs per weight fragment) and in 8 bits (x is converted again for every tile);
+// the GEMM likes many row blocks, which need no sums over clusters.
+// Measured, mma.sync against GEMM, us: 8 tokens 8192 x 8192 11.9 / 13.0, 5120 x
+// 10240 12.7 / 10.9, 2048 x 40000 18.6 / 16.5; 8 bits 2048 x 8192 5.7 / 6.1, 4096
+// x 8192 8.4 / 7.7 (exact by contract), 8192 x 8192 14.8 / 13.2; 16 tokens 2048 x
+// 8192 6.1 / 6.4, 4096 x 4096 7.1 / 6.6; 8 bits 2048 x 2048 5.7 / 5.2, 2048 x
+// 8192 8.0 / 6.4.
 bool use_gemm(const moe_linear* L, const XIn& in, int T) {
   const long long weights = (long long)L->w.N * L->w.K;
   if (T > kSmallTokens) return true;
   if (T > 8) return weights > (in.x ? 16000000ll : kGemmWeights9);
-  if (T > (in.x ? 1 : kDotTokensQ8)) return weights > (in.x ? 80000000ll : kGemmWeights2);
+  if (T > (in.x ? 1 : kDotTokensQ8))
+    return weights > (!in.x ? kGemmWeights2 : L->w.N > L->w.K ? 48000000ll : 80000000ll);
   return false;
 }
 

@@ -31,7 +31,8 @@ constexpr int kTileBytes = 1152;
 constexpr int kDotTokensQ8 = 2;   // largest 8-bit batch of the dot-product kernel
 constexpr int kSmallTokens = 16;  // largest batch of the small-batch kernels
 // fewest weights (N x K) that take the GEMM with 9 to 16 and with 2 to 8 tokens
-constexpr long long kGemmWeights9 = 8000000, kGemmWeights2 = 1 << 25;
+// (of 2 to 8 tokens, fewer are exact by the entry points' contract)
+constexpr long long kGemmWeights9 = 4000000, kGemmWeights2 = 1 << 25;
 
 // Largest token tile of the GEMM (no CTA has a second one).
 constexpr int kMaxOneTile = 224;

@@ -67,6 +67,23 @@ def test_large_batches(cuda_device, T, N, K, bias):
     assert moe.moe_linear_status_sync(lin.handle) == moe.MOE_OK
 
 
+# either side of the sizes where the GEMM takes over from the small-batch kernels,
+# on handles made for just that batch
+@pytest.mark.parametrize("T,N,K,q8", [(2, 9380, 5120, False), (8, 9370, 5120, False), (3, 16400, 2080, True), (8, 16100, 2080, True),
+                                      (9, 1960, 2048, True), (16, 1940, 2048, True), (9, 7820, 2048, False), (16, 7800, 2048, False)])
+def test_path_borders(cuda_device, T, N, K, q8):
+    lin, w, b = make(N, K, T, True, cuda_device)
+    if q8:
+        g = torch.Generator().manual_seed(T + N + K)
+        q = torch.randint(-127, 128, (T, K), generator=g).to(torch.int8)
+        s = torch.rand(T, K // 32, generator=g) + 0.01
+        check(lin.forward_q8(q.to(cuda_device), s.to(cuda_device)), R.q8_values(q, s), w, b, bf16=False)
+    else:
+        x = acts(T, K)
+        check(lin.forward(x.to(cuda_device)), x.double(), w, b)
+    assert moe.moe_linear_status_sync(lin.handle) == moe.MOE_OK
+
+
 # one tile per SM and few row blocks: tiles of more than 160 tokens, whole and
 # shared by the CTAs of a cluster, with rows and tokens left over
 @pytest.mark.parametrize("T,N,K", [(322, 7700, 352), (161, 1600, 6752), (700, 2044, 8192), (213, 1500, 6784)])
