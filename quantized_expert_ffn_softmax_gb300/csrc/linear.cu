@@ -6,7 +6,7 @@
 // bounds these kernels is the number of instructions per weight, first of all
 // the unpacking on the integer pipe.
 //   dot_kernel    1 token in bf16, up to 2 in 8 bits: integer dot products
-//                 (dp4a) of the codes with x as integers
+//                 (dp2a, dp4a) of the codes with x as integers
 //   small_kernel  up to 16 tokens: the legacy tensor path (mma.sync), W the
 //                 16-row operand A unpacked exactly to bf16 integers, up to two
 //                 8-token column tiles operand B
@@ -218,7 +218,8 @@ struct Stream {
 // x as integers, per block of 32: 8-bit x as it is; bf16 x as q * 2^(e - 13)
 // with 2^e <= max|x| < 2^(e + 1) over the block, so that every value down to
 // 1/64 of the block's largest is exact and smaller ones are off by 2^(e - 14)
-// at most; |q| <= 16320 = 256 hi + lo with hi and lo in 8 bits.
+// at most; |q| <= 16320, pairs for dp2a (as two planes of bytes for dp4a, with
+// one more instruction to join the sums, 1 x 2048-131073 took 26.1 us, not 25.2).
 // A lane holds eight inputs of two rows of a block per step: their dot product
 // with the codes is exact in 32 bits; the -8 of the codes and the bits that
 // make the integer a float (2^23 + 2^22 as an exponent) ride on the
@@ -227,7 +228,7 @@ constexpr int kFloatBias = 0x4B400000;  // 12582912.0f
 template <int TT, int MT, int ST, int kCtas, bool kQ8>
 __global__ void __launch_bounds__(256, kCtas) dot_kernel(const __grid_constant__ SmallParams p, int S) {
   extern __shared__ __align__(128) unsigned char smem[];
-  using Planes = typename std::conditional<kQ8, uint2, uint4>::type;  // codes, or hi and lo
+  using Planes = typename std::conditional<kQ8, uint2, uint4>::type;  // bytes, or pairs of 16 bits
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, K = p.w.K;
   Stream<MT, ST> in(p.w, S, smem);
   const int nv = p.w.kc * (kTileK / 8);  // vectors of 8 inputs, past K zeros
@@ -240,16 +241,15 @@ __global__ void __launch_bounds__(256, kCtas) dot_kernel(const __grid_constant__
   for (int i0 = 0; i0 < TT * nv; i0 += 256) {  // (nv is a multiple of 4: blocks are four neighbouring lanes)
     const int i = i0 + threadIdx.x, tok = i / nv, v = i - tok * nv;
     const bool here = tok < min(p.T, TT) && 8 * v < K;
-    // inputs 2 j in the low, 2 j + 1 in the high nibbles' order of dp4a
-    constexpr int kPos[8] = {0, 4, 1, 5, 2, 6, 3, 7};
+    // bytes of the even nibbles are inputs 0, 4, 1, 5, of the odd ones 2, 6, 3, 7
     float scale;
     int sum = 0;
-    uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+    uint32_t c8[2], c16[4];
     if constexpr (kQ8) {
       uint2 c = make_uint2(0u, 0u);
       if (here) c = *reinterpret_cast<const uint2*>(p.q + (size_t)tok * K + 8 * v);
       scale = here ? ld_f32(p.qs + (size_t)tok * (K >> 5) + (v >> 2)) : 0.0f;
-      hi[0] = __byte_perm(c.x, c.y, 0x5140), hi[1] = __byte_perm(c.x, c.y, 0x7362);
+      c8[0] = __byte_perm(c.x, c.y, 0x5140), c8[1] = __byte_perm(c.x, c.y, 0x7362);
       sum = __dp4a((int)c.x, 0x01010101, __dp4a((int)c.y, 0x01010101, 0));
     } else {
       uint4 c = make_uint4(0u, 0u, 0u, 0u);
@@ -265,19 +265,17 @@ __global__ void __launch_bounds__(256, kCtas) dot_kernel(const __grid_constant__
       const float up = finite ? pow2f(13 - e) : 0.0f;
       scale = finite ? pow2f(e - 13) : __uint_as_float(0x7fffffffu);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int qv = finite ? __float2int_rn(f[kPos[j]] * up) : 0;
-        const int h = (qv + 128) >> 8, l = qv - 256 * h;
-        sum += qv;
-        hi[j >> 2] |= (uint32_t)(h & 0xff) << (8 * (j & 3));
-        lo[j >> 2] |= (uint32_t)(l & 0xff) << (8 * (j & 3));
+      for (int j = 0; j < 4; ++j) {
+        const int q0 = finite ? __float2int_rn(f[j] * up) : 0, q1 = finite ? __float2int_rn(f[j + 4] * up) : 0;
+        sum += q0 + q1;
+        c16[j] = __byte_perm((uint32_t)q0, (uint32_t)q1, 0x5410);
       }
     }
     if (i >= TT * nv) continue;
     if constexpr (kQ8)
-      planes[i] = make_uint2(hi[0], hi[1]);
+      planes[i] = make_uint2(c8[0], c8[1]);
     else
-      planes[i] = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+      planes[i] = make_uint4(c16[0], c16[1], c16[2], c16[3]);
     meta[i] = make_int2(__float_as_int(scale), kFloatBias - 8 * sum);
   }
   __syncthreads();
@@ -334,8 +332,8 @@ __global__ void __launch_bounds__(256, kCtas) dot_kernel(const __grid_constant__
                 if constexpr (kQ8) {
                   d = __dp4a(we, (int)px[k].x, __dp4a(wo, (int)px[k].y, mx[k].y));
                 } else {
-                  const int h = __dp4a(we, (int)px[k].x, __dp4a(wo, (int)px[k].y, 0));
-                  d = h * 256 + __dp4a(we, (int)px[k].z, __dp4a(wo, (int)px[k].w, mx[k].y));
+                  d = __dp2a_lo((int)px[k].x, we, __dp2a_lo((int)px[k].z, wo, mx[k].y));
+                  d = __dp2a_hi((int)px[k].y, we, __dp2a_hi((int)px[k].w, wo, d));
                 }
                 const float v = __int_as_float(d) - __int_as_float(kFloatBias);
                 acc[m][k][r] = fmaf(v, sr[r] * __int_as_float(mx[k].x), acc[m][k][r]);
@@ -572,8 +570,8 @@ struct Variant {
 };
 
 // A kernel variant; `call` is what to do with it.  Dot products: one tile per
-// unit at two CTAs per SM, with eight stages while both fit beside x (26 us at
-// 1 x 2048-131073; measured before other steps: two tiles 29.9 us, six stages at
+// unit at two CTAs per SM, with eight stages while both fit beside x (25.2 us
+// at 1 x 2048-131073; measured before other steps: two tiles 29.9 us, six stages at
 // three CTAs 30.1, this 28.3), else with four.
 template <int TT, int ST, bool kQ8, typename F>
 cudaError_t with_dot(F&& call) {
