@@ -546,8 +546,9 @@ __global__ void __launch_bounds__(256, kCtas) small_kernel(const __grid_constant
 }
 
 // Warps per unit: the smallest power of two whose last round of units leaves
-// at most 1/16 of the warps idle, else the one that leaves fewest.
-int warps_per_unit(int units, int kc, int slots) {
+// at most 1/16 of the warps idle, else the one that leaves fewest; and the part
+// of the warps that it keeps busy.
+int warps_per_unit(int units, int kc, int slots, double* busy = nullptr) {
   int S = 1;
   double best = 0.0;
   for (int c = 1; c <= 8 && c <= kc; c *= 2) {
@@ -556,11 +557,13 @@ int warps_per_unit(int units, int kc, int slots) {
     if (used > best) S = c, best = used;
     if (best > 0.9375) break;
   }
+  if (busy) *busy = best;
   return S;
 }
 
 constexpr int kDotSmem = 64 * 1024;  // largest x area of dot_kernel
-constexpr int kDotDeep = 36 * 1024;  // largest with eight stages (two CTAs in 227 KB)
+constexpr int kDotDeep = 36 * 1024;  // largest with eight tiles in a warp's ring (two CTAs in 227 KB)
+constexpr int kDotTen = 21 * 1024;   // largest with ten
 
 template <int MT, int ST, int kCtas>
 struct Variant {
@@ -569,15 +572,32 @@ struct Variant {
   int part;     // bytes of the partial sums when warps share a unit
 };
 
-// A kernel variant; `call` is what to do with it.  Dot products: one tile per
-// unit at two CTAs per SM, with eight stages while both fit beside x (25.2 us
-// at 1 x 2048-131073; measured before other steps: two tiles 29.9 us, six stages at
-// three CTAs 30.1, this 28.3), else with four.
-template <int TT, int ST, bool kQ8, typename F>
+// A kernel variant; `call` is what to do with it.
+template <int TT, int MT, int ST, bool kQ8, typename F>
 cudaError_t with_dot(F&& call) {
-  constexpr int MT = 1, kCtas = 2;
+  constexpr int kCtas = 2;
   return call(Variant<MT, ST, kCtas>{dot_kernel<TT, MT, ST, kCtas, kQ8>, kDotSmem, 8 * MT * TT * 64});
 }
+// Two tiles per unit (one token) share the loads of x, in a ring as deep as fits
+// beside x with two CTAs per SM, where there are tiles enough to keep as many
+// warps busy (1 x 2048-131073: 24.0 us, with one tile 25.2; three tiles 24.2;
+// three CTAs per SM 25.0.  1 x 2048-2048: 2.5, with one tile 2.3; 1 x 5120-10240,
+// 53 % of the warps busy instead of 70: 9.4 and 7.5).
+bool two_tiles(const Weights& w, int num_sms) {
+  if (w.nt < 2 * num_sms) return false;
+  double one, two;
+  warps_per_unit(w.nt, w.kc, 16 * num_sms, &one);
+  warps_per_unit((w.nt + 1) / 2, w.kc, 16 * num_sms, &two);
+  return two >= 0.85 * one;
+}
+template <int TT, bool kQ8, typename F>
+cudaError_t pick_dot(int x_bytes, bool two, F&& call) {
+  if (x_bytes > kDotDeep) return with_dot<TT, 1, 4, kQ8>(call);
+  if constexpr (TT == 1)
+    if (two) return x_bytes > kDotTen ? with_dot<TT, 2, 4, kQ8>(call) : with_dot<TT, 2, 5, kQ8>(call);
+  return with_dot<TT, 1, 8, kQ8>(call);
+}
+
 template <int NT, int MT, int ST, bool kQ8, typename F>
 cudaError_t with_small(F&& call) {
   constexpr int kCtas = 2;
@@ -593,12 +613,13 @@ struct SetSmem {
 };
 // The shared-memory limits of every variant, on the current device.
 cudaError_t small_init() {
-  cudaError_t e = with_dot<1, 8, false>(SetSmem());
-  if (e == cudaSuccess) e = with_dot<1, 4, false>(SetSmem());
-  if (e == cudaSuccess) e = with_dot<1, 8, true>(SetSmem());
-  if (e == cudaSuccess) e = with_dot<1, 4, true>(SetSmem());
-  if (e == cudaSuccess) e = with_dot<2, 8, true>(SetSmem());
-  if (e == cudaSuccess) e = with_dot<2, 4, true>(SetSmem());
+  cudaError_t e = cudaSuccess;
+  for (int x_bytes : {kDotTen, kDotDeep, kDotSmem})
+    for (int two = 0; two < 2; ++two) {
+      if (e == cudaSuccess) e = pick_dot<1, false>(x_bytes, two, SetSmem());
+      if (e == cudaSuccess) e = pick_dot<1, true>(x_bytes, two, SetSmem());
+      if (e == cudaSuccess) e = pick_dot<2, true>(x_bytes, two, SetSmem());
+    }
   if (e == cudaSuccess) e = with_small<1, 1, 8, false>(SetSmem());
   if (e == cudaSuccess) e = with_small<1, 2, 4, false>(SetSmem());
   if (e == cudaSuccess) e = with_small<2, 2, 4, false>(SetSmem());
@@ -630,10 +651,9 @@ cudaError_t launch_small(const SmallParams& p, int num_sms, cudaStream_t s) {
   if (p.T <= (kQ8 ? kDotTokensQ8 : 1) && x_bytes <= kDotSmem) {
     prof::Scope scope(kQ8 ? "linear_dot_q8" : "linear_dot", s);
     const Launch go{p, x_bytes, num_sms, s};
-    const bool deep = x_bytes <= kDotDeep;
     if constexpr (kQ8)
-      if (p.T == 2) return deep ? with_dot<2, 8, true>(go) : with_dot<2, 4, true>(go);
-    return deep ? with_dot<1, 8, kQ8>(go) : with_dot<1, 4, kQ8>(go);
+      if (p.T == 2) return pick_dot<2, true>(x_bytes, false, go);
+    return pick_dot<1, kQ8>(x_bytes, two_tiles(p.w, num_sms), go);
   }
   prof::Scope scope(kQ8 ? "linear_small_q8" : "linear_small", s);
   const Launch go{p, 0, num_sms, s};

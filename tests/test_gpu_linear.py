@@ -84,6 +84,26 @@ def test_path_borders(cuda_device, T, N, K, q8):
     assert moe.moe_linear_status_sync(lin.handle) == moe.MOE_OK
 
 
+# one token, many rows: two row tiles per unit (an odd number of tiles, a last one
+# with one row), with x small, large and larger than what they are used for
+@pytest.mark.parametrize("N,K", [(4897, 96), (4897, 2080), (4900, 7200), (4897, 8224), (5020, 12288), (4897, 12320), (40000, 512)])
+@pytest.mark.parametrize("q8", [False, True])
+def test_one_token_many_rows(cuda_device, N, K, q8):
+    lin, w, b = make(N, K, 1, True, cuda_device)
+    y = torch.full((2, N), 7.0, dtype=torch.bfloat16, device=cuda_device)
+    if q8:
+        g = torch.Generator().manual_seed(N + K)
+        q = torch.randint(-127, 128, (1, K), generator=g).to(torch.int8)
+        s = torch.rand(1, K // 32, generator=g) + 0.01
+        moe.moe_linear_forward_q8(lin.handle, q.to(cuda_device), s.to(cuda_device), 1, y[:1])
+        check(y[:1], R.q8_values(q, s), w, b, bf16=False)
+    else:
+        x = acts(1, K)
+        moe.moe_linear_forward(lin.handle, x.to(cuda_device), 1, y[:1])
+        check(y[:1], x.double(), w, b)
+    assert (y[1] == 7.0).all()
+
+
 # one tile per SM and few row blocks: tiles of more than 160 tokens, whole and
 # shared by the CTAs of a cluster, with rows and tokens left over
 @pytest.mark.parametrize("T,N,K", [(322, 7700, 352), (161, 1600, 6752), (700, 2044, 8192), (213, 1500, 6784)])
