@@ -456,6 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       st += kTurns;
       if (st >= S) st -= S, par ^= 1;
     }
+    if (KS > 1) dep_wait();  // (a group without a stage: the sum over a cluster writes y)
   } else if (warp == kRawWarp) {
     // ------------------------------------------------------------ packed tiles
     dep_wait();

@@ -390,6 +390,37 @@ def test_bounded_waits_report_a_timeout(cuda_device, monkeypatch, T, N, K):
     assert moe.moe_linear_status_sync(lin.handle) == moe.MOE_OK
 
 
+@pytest.mark.parametrize("T,N,K", [(32, 1030, 4096), (40, 1000, 512), (700, 2044, 8192)])
+def test_bounded_waits_in_clusters(cuda_device, monkeypatch, T, N, K):
+    """The same where the CTAs of a cluster share a tile: all of them end."""
+    test_bounded_waits_report_a_timeout(cuda_device, monkeypatch, T, N, K)
+
+
+@pytest.mark.parametrize("T,N,K", [(20, 500, 512), (64, 2000, 256), (33, 900, 1056), (50, 300, 768)])
+def test_few_stages_back_to_back(cuda_device, T, N, K):
+    """More groups of producers than stages; every call reads the output of the
+    one before it and overwrites what the one before that read."""
+    a, wa, ba = make(N, K, T, True, cuda_device)
+    b, wb, bb = make(K, N // 32 * 32, T, True, cuda_device, seed=1)
+    x0 = acts(T, K).to(cuda_device)
+    x = x0.clone()
+    y = torch.empty(T, N, dtype=torch.bfloat16, device=cuda_device)
+    cut = torch.empty(T, N // 32 * 32, dtype=torch.bfloat16, device=cuda_device)
+    want, w = [], x0
+    for _ in range(3):
+        w = b.forward(a.forward(w)[:, :cut.shape[1]].contiguous())
+        torch.cuda.synchronize()
+        want.append(w)
+    for r in range(20):
+        x.copy_(x0)
+        for i in range(3):
+            moe.moe_linear_forward(a.handle, x, T, y)
+            cut.copy_(y[:, :cut.shape[1]])
+            moe.moe_linear_forward(b.handle, cut, T, x)
+            assert r < 19 or torch.equal(x, want[i])
+    check(y, want[1].double().cpu(), wa, ba)
+
+
 @pytest.mark.parametrize("T", [1, 4, 32, 200])
 def test_side_stream_and_graph(cuda_device, T):
     N, K = 1536, 2048
