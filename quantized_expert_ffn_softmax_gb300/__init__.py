@@ -133,13 +133,12 @@ def _ptr(a) -> Optional[int]:
     if a is None:
         return None
     try:  # a tensor, first: every argument of a decode-sized call counts
-        p = a.data_ptr()
+        if a.is_contiguous():
+            return a.data_ptr()
     except AttributeError:
         pass
     else:
-        if not a.is_contiguous():
-            raise ValueError("tensor must be contiguous")
-        return p
+        raise ValueError("tensor must be contiguous")
     if isinstance(a, int):
         return a
     if hasattr(a, "ctypes"):
